@@ -34,6 +34,8 @@ EXPORTS = (
     "binattn_ref_bf16_forward_workspace_bytes", "binattn_ref_bf16_forward_ws",
     "binattn_forward_sample_bias_workspace_bytes", "binattn_forward_sample_bias_ws",
     "binattn_backward_workspace_bytes", "binattn_backward",
+    "binattn_norm_rope", "binattn_norm_rope_pack",
+    "binattn_norm_rope_backward_workspace_bytes", "binattn_norm_rope_backward",
 )
 
 
@@ -81,6 +83,15 @@ def lib() -> ctypes.CDLL:
     L.binattn_backward_workspace_bytes.restype = ctypes.c_size_t
     L.binattn_backward.argtypes = [P, P, P, P, P, P, P, F, I, I, I, I, P, P, P, P, P, ctypes.c_size_t, P]
     L.binattn_backward.restype = I
+    L.binattn_norm_rope.argtypes = [P, P, I, P, P, P, P, P, I, I, I, F, I, I, I, I, P, P, P]
+    L.binattn_norm_rope.restype = I
+    L.binattn_norm_rope_pack.argtypes = [P, P, I, P, P, P, P, P, I, I, I, F, I, I, I, I, P, P, P, P, P]
+    L.binattn_norm_rope_pack.restype = I
+    L.binattn_norm_rope_backward_workspace_bytes.argtypes = [I, I, I, I]
+    L.binattn_norm_rope_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.binattn_norm_rope_backward.argtypes = [P, P, I, P, P, P, I, P, P, P, P, I, I, I, F, I, I, I, I, P, P, P, P, P, P,
+                                             ctypes.c_size_t, P]
+    L.binattn_norm_rope_backward.restype = I
     L.binattn_quantize_v.argtypes = [P, I, I, I, I, P, P, P]
     L.binattn_quantize_v.restype = I
     L.binattn_forward_int8_workspace_bytes.argtypes = [I, I, I, I, I]
@@ -369,6 +380,151 @@ def backward(q_bits: torch.Tensor, k_bits: torch.Tensor, alpha_q: torch.Tensor, 
                                       _ptr(dbias), _ptr(workspace), ctypes.c_size_t(size), _stream(stream, dev)),
                "binattn_backward")
     return dV, ds, dt, dbias
+
+
+def rope_tables(positions: torch.Tensor, rot: int, theta: float = 10000.0):
+    """cos and sin tables (fp32 [..., N, rot / 2]) of a rotation by position for
+    norm_rope: pair p of axis a turns by positions[..., a] * theta^(-p / pairs),
+    pairs = rot / 2 / axes pairs per axis, axis by axis. positions: [N], or
+    [N, axes] / [B, N, axes] (a patch grid has two axes). Angles are taken in 64
+    bits. Plain torch: it is done once, not per call."""
+    pos = positions.to(torch.float64)
+    if pos.dim() == 1:
+        pos = pos[:, None]
+    axes = pos.shape[-1]
+    if rot < 0 or rot % (2 * axes):
+        raise ValueError(f"rot = {rot} does not split into pairs over {axes} axes")
+    pairs = rot // 2 // axes
+    freq = float(theta) ** (-torch.arange(pairs, dtype=torch.float64, device=pos.device) / max(pairs, 1))
+    ang = (pos[..., None] * freq).flatten(-2)
+    return ang.cos().float(), ang.sin().float()
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtypes) -> list[int]:
+    """Batch, head and token stride of a [B, H, N, d] view with contiguous rows."""
+    _expect(t, name, shape, dtypes)
+    if shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous (its last stride is {t.stride(3)})")
+    return [t.stride(i) for i in range(3)]
+
+
+def _strides(*rows: list[int]):
+    flat = [s for r in rows for s in r]
+    return (ctypes.c_int64 * len(flat))(*flat)
+
+
+def _raw(t: torch.Tensor):
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _on(stream, dev: torch.device):
+    """Allocations of a call that runs on `stream` come from that stream's pool,
+    so that what the call frees again is not handed to another stream meanwhile."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev))
+
+
+def _norm_rope_args(q, k, w_q, w_k, cos, sin):
+    """Checks the norm_rope calls share; returns what the ABI takes of them."""
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, H, N, d], got {tuple(q.shape)}")
+    B, H, N, d = q.shape
+    dt = {torch.float32: F32, torch.bfloat16: BF16}.get(q.dtype)
+    if dt is None:
+        raise TypeError(f"norm_rope takes float32 or bfloat16, got {q.dtype}")
+    strides = _strides(_rows(q, "q", (B, H, N, d), (q.dtype,)), _rows(k, "k", (B, H, N, d), (q.dtype,)))
+    for name, w in (("w_q", w_q), ("w_k", w_k)):
+        _expect(w, name, (d,), (torch.float32,))
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    rot, per_batch = 0, False
+    if cos is not None:
+        per_batch = cos.dim() == 3
+        rot = 2 * cos.shape[-1]
+        shape = ((B,) if per_batch else ()) + (N, rot // 2)
+        _expect(cos, "cos", shape, (torch.float32,))
+        _expect(sin, "sin", shape, (torch.float32,))
+    if rot == 0:
+        cos = sin = None
+    return (B, H, N, d), dt, strides, cos, sin, rot, per_batch
+
+
+def norm_rope(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor | None, w_k: torch.Tensor | None,
+              cos: torch.Tensor | None, sin: torch.Tensor | None, eps: float = 1e-6, interleaved: bool = False,
+              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """RMS norm of every row of q and k [B,H,N,d] (float32 or bfloat16; any view
+    with contiguous rows, e.g. of a fused projection's output), times w_q / w_k
+    (fp32 [d] or None), its channel pairs turned by cos / sin (fp32 [N, rot / 2] or
+    [B, N, rot / 2], see rope_tables; None: no rotation). interleaved: pairs
+    (2p, 2p + 1) instead of (p, p + rot / 2). Returns (q_out, k_out), contiguous."""
+    (B, H, N, d), dt, strides, cos, sin, rot, per_batch = _norm_rope_args(q, k, w_q, w_k, cos, sin)
+    for name, t in (("q_out", q_out), ("k_out", k_out)):
+        _expect(t, name, (B, H, N, d), (q.dtype,))
+    dev = _device(q, k, w_q, w_k, cos, sin, q_out, k_out)
+    with torch.cuda.device(dev):
+        with _on(stream, dev):
+            q_out, k_out = (torch.empty((B, H, N, d), dtype=q.dtype, device=dev) if t is None else t
+                            for t in (q_out, k_out))
+        _check(lib().binattn_norm_rope(_raw(q), _raw(k), dt, strides, _ptr(w_q), _ptr(w_k), _ptr(cos), _ptr(sin), rot,
+                                       int(per_batch), int(bool(interleaved)), float(eps), B, H, N, d, _ptr(q_out),
+                                       _ptr(k_out), _stream(stream, dev)), "binattn_norm_rope")
+    return q_out, k_out
+
+
+def norm_rope_pack(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor | None, w_k: torch.Tensor | None,
+                   cos: torch.Tensor | None, sin: torch.Tensor | None, eps: float = 1e-6, interleaved: bool = False,
+                   stream=None):
+    """norm_rope ended in pack's output, in one pass: (q_bits, alpha_q, k_bits,
+    alpha_k), the binary forward's inputs. Arguments as norm_rope."""
+    (B, H, N, d), dt, strides, cos, sin, rot, per_batch = _norm_rope_args(q, k, w_q, w_k, cos, sin)
+    dev = _device(q, k, w_q, w_k, cos, sin)
+    with torch.cuda.device(dev):
+        with _on(stream, dev):
+            bits = [torch.empty((B, H, N, _words(d)), dtype=torch.int32, device=dev) for _ in range(2)]
+            alpha = [torch.empty((B, H, N), dtype=torch.float32, device=dev) for _ in range(2)]
+        _check(lib().binattn_norm_rope_pack(_raw(q), _raw(k), dt, strides, _ptr(w_q), _ptr(w_k), _ptr(cos), _ptr(sin),
+                                            rot, int(per_batch), int(bool(interleaved)), float(eps), B, H, N, d,
+                                            _ptr(bits[0]), _ptr(alpha[0]), _ptr(bits[1]), _ptr(alpha[1]),
+                                            _stream(stream, dev)), "binattn_norm_rope_pack")
+    return bits[0], alpha[0], bits[1], alpha[1]
+
+
+def norm_rope_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
+                       w_q: torch.Tensor | None, w_k: torch.Tensor | None, cos: torch.Tensor | None,
+                       sin: torch.Tensor | None, eps: float = 1e-6, interleaved: bool = False,
+                       dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of norm_rope for upstream gradients dq_out, dk_out of its outputs
+    ([B,H,N,d], float32 or bfloat16, both alike): (dq, dk, dw_q, dw_k). dq and dk
+    have q's type and may be given as views with contiguous rows (e.g. of the
+    projection's gradient); dw is fp32 [d], None where w is None."""
+    (B, H, N, d), dt, strides, cos, sin, rot, per_batch = _norm_rope_args(q, k, w_q, w_k, cos, sin)
+    gdt = {torch.float32: F32, torch.bfloat16: BF16}.get(dq_out.dtype)
+    if gdt is None:
+        raise TypeError(f"the upstream gradients must be float32 or bfloat16, got {dq_out.dtype}")
+    _expect(dq_out, "dq_out", (B, H, N, d), (dq_out.dtype,))
+    _expect(dk_out, "dk_out", (B, H, N, d), (dq_out.dtype,))
+    for name, t in (("dq", dq), ("dk", dk)):
+        if t is not None:
+            _rows(t, name, (B, H, N, d), (q.dtype,))
+    dev = _device(q, k, w_q, w_k, cos, sin, dq_out, dk_out, dq, dk, workspace)
+    need = 0 if w_q is None and w_k is None else int(lib().binattn_norm_rope_backward_workspace_bytes(B, H, N, d))
+    with torch.cuda.device(dev):
+        with _on(stream, dev):
+            dq, dk = (torch.empty((B, H, N, d), dtype=q.dtype, device=dev) if t is None else t for t in (dq, dk))
+            dw_q, dw_k = (None if w is None else torch.empty(d, dtype=torch.float32, device=dev) for w in (w_q, w_k))
+            if workspace is None and need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        gstrides = _strides(_rows(dq, "dq", (B, H, N, d), (q.dtype,)), _rows(dk, "dk", (B, H, N, d), (q.dtype,)))
+        _check(lib().binattn_norm_rope_backward(_raw(q), _raw(k), dt, strides, _ptr(dq_out), _ptr(dk_out), gdt,
+                                                _ptr(w_q), _ptr(w_k), _ptr(cos), _ptr(sin), rot, int(per_batch),
+                                                int(bool(interleaved)), float(eps), B, H, N, d, _raw(dq), _raw(dk),
+                                                gstrides, _ptr(dw_q), _ptr(dw_k), _ptr(workspace),
+                                                ctypes.c_size_t(size), _stream(stream, dev)),
+               "binattn_norm_rope_backward")
+    return dq, dk, dw_q, dw_k
 
 
 def quantize_v(v: torch.Tensor, stream=None):

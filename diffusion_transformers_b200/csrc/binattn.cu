@@ -17,6 +17,7 @@
 #include "fwd_tc2.cuh"
 #include "quantv.cuh"
 #include "bwd_simt.cuh"
+#include "norm_rope.cuh"
 
 namespace {
 
@@ -703,6 +704,181 @@ int binattn_backward(const uint32_t* q_bits, const uint32_t* k_bits, const float
   if (binattn::bwd::backward(q_bits, k_bits, alpha_q, alpha_k, bias, v, dO, softmax_scale, B, H, N, d, dV, ds, dt,
                              dbias, lse, D, static_cast<cudaStream_t>(stream), &msg))
     return fail(BINATTN_ERR_CUDA, "%s", msg.c_str());
+  return ok();
+}
+
+namespace {
+// Strides {batch, head, token} of q then of k (host array of 6, elements; null:
+// contiguous [B,H,N,d]) into the kernel's fields. A dimension of size 1 is never
+// stepped over, so its stride is dropped.
+int nr_strides(const int64_t* strides, int B, int H, int N, int d, const char* what, long long* sb, long long* sh,
+               long long* sn) {
+  for (int t = 0; t < 2; ++t) {
+    const int64_t* s = strides ? strides + 3 * t : nullptr;
+    sb[t] = B == 1 ? 0 : s ? s[0] : static_cast<long long>(H) * N * d;
+    sh[t] = H == 1 ? 0 : s ? s[1] : static_cast<long long>(N) * d;
+    sn[t] = N == 1 ? 0 : s ? s[2] : d;
+    if (sb[t] < 0 || sh[t] < 0 || sn[t] < 0) return fail(BINATTN_ERR_ARG, "%s has a negative stride", what);
+  }
+  return BINATTN_OK;
+}
+
+// Whether no two rows of d elements at these strides share an element.
+bool nr_disjoint(long long sb, long long sh, long long sn, int B, int H, int N, int d) {
+  long long st[3] = {sb, sh, sn};
+  int size[3] = {B, H, N};
+  long long span = d;  // elements from the first to the last of the dimensions so far
+  bool used[3] = {false, false, false};
+  for (int k = 0; k < 3; ++k) {
+    int best = -1;
+    for (int e = 0; e < 3; ++e)
+      if (!used[e] && (best < 0 || st[e] < st[best])) best = e;
+    used[best] = true;
+    if (size[best] == 1) continue;
+    if (st[best] < span) return false;
+    span += st[best] * (size[best] - 1);
+  }
+  return true;
+}
+
+// The arguments the three norm_rope calls share, checked and laid out.
+int nr_params(const void* q, const void* k, int dtype, const int64_t* strides, const float* w_q, const float* w_k,
+              const float* cos, const float* sin, int rot, int per_batch, float eps, int B, int H, int N, int d,
+              binattn::nr::Params* p) {
+  if (!q) return fail(BINATTN_ERR_NULL, "q is NULL");
+  if (!k) return fail(BINATTN_ERR_NULL, "k is NULL");
+  if (dtype != BINATTN_F32 && dtype != BINATTN_BF16)
+    return fail(BINATTN_ERR_DTYPE, "dtype %d is neither BINATTN_F32 nor BINATTN_BF16", dtype);
+  if (int rc = check_shape(B, H, N, d)) return rc;
+  const uintptr_t es = dtype == BINATTN_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(q) % es || reinterpret_cast<uintptr_t>(k) % es)
+    return fail(BINATTN_ERR_ALIGN, "q or k is not aligned to its element");
+  if (w_q && !aligned16(w_q)) return fail(BINATTN_ERR_ALIGN, "w_q is not 16-byte aligned");
+  if (w_k && !aligned16(w_k)) return fail(BINATTN_ERR_ALIGN, "w_k is not 16-byte aligned");
+  if (rot < 0 || rot > d || rot % 2) return fail(BINATTN_ERR_SHAPE, "rot = %d is not an even number in [0, d = %d]", rot, d);
+  if (rot) {
+    BINATTN_CHECK_PTR(cos);
+    BINATTN_CHECK_PTR(sin);
+  }
+  if (!std::isfinite(eps) || eps < 1e-30f) return fail(BINATTN_ERR_ARG, "eps = %g is not a positive number", eps);
+  std::memset(p, 0, sizeof *p);
+  p->x[0] = q;
+  p->x[1] = k;
+  if (int rc = nr_strides(strides, B, H, N, d, "q or k", p->xb, p->xh, p->xn)) return rc;
+  p->w[0] = w_q;
+  p->w[1] = w_k;
+  p->cosv = cos;
+  p->sinv = sin;
+  p->R = rot;
+  p->per_batch = per_batch != 0;
+  p->eps = eps;
+  p->B = B;
+  p->H = H;
+  p->N = N;
+  p->d = d;
+  return BINATTN_OK;
+}
+}  // namespace
+
+int binattn_norm_rope(const void* q, const void* k, int dtype, const int64_t* strides, const float* w_q,
+                      const float* w_k, const float* cos, const float* sin, int rot, int per_batch, int interleaved,
+                      float eps, int B, int H, int N, int d, void* q_out, void* k_out, void* stream) {
+  namespace nr = binattn::nr;
+  nr::Params p;
+  if (int rc = nr_params(q, k, dtype, strides, w_q, w_k, cos, sin, rot, per_batch, eps, B, H, N, d, &p)) return rc;
+  BINATTN_CHECK_PTR(q_out);
+  BINATTN_CHECK_PTR(k_out);
+  p.out[0] = q_out;
+  p.out[1] = k_out;
+  if (int rc = nr_strides(nullptr, B, H, N, d, "out", p.ob, p.oh, p.on)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = dtype == BINATTN_F32;
+  const bool vec = nr::vec_ok(p, f32 ? 4 : 2, 0, false);
+  if (f32) nr::launch<float, float, nr::kOpOut>(p, interleaved != 0, vec, st);
+  else nr::launch<uint16_t, uint16_t, nr::kOpOut>(p, interleaved != 0, vec, st);
+  return launch_status("norm_rope kernel");
+}
+
+int binattn_norm_rope_pack(const void* q, const void* k, int dtype, const int64_t* strides, const float* w_q,
+                           const float* w_k, const float* cos, const float* sin, int rot, int per_batch,
+                           int interleaved, float eps, int B, int H, int N, int d, uint32_t* q_bits, float* alpha_q,
+                           uint32_t* k_bits, float* alpha_k, void* stream) {
+  namespace nr = binattn::nr;
+  nr::Params p;
+  if (int rc = nr_params(q, k, dtype, strides, w_q, w_k, cos, sin, rot, per_batch, eps, B, H, N, d, &p)) return rc;
+  BINATTN_CHECK_PTR(q_bits);
+  BINATTN_CHECK_PTR(alpha_q);
+  BINATTN_CHECK_PTR(k_bits);
+  BINATTN_CHECK_PTR(alpha_k);
+  p.bits[0] = q_bits;
+  p.bits[1] = k_bits;
+  p.alpha[0] = alpha_q;
+  p.alpha[1] = alpha_k;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = dtype == BINATTN_F32;
+  const bool vec = nr::vec_ok(p, f32 ? 4 : 2, 0, false);
+  if (f32) nr::launch<float, float, nr::kOpPack>(p, interleaved != 0, vec, st);
+  else nr::launch<uint16_t, uint16_t, nr::kOpPack>(p, interleaved != 0, vec, st);
+  return launch_status("norm_rope_pack kernel");
+}
+
+size_t binattn_norm_rope_backward_workspace_bytes(int B, int H, int N, int d) {
+  if (B < 1 || H < 1 || N < 1 || d < 1 || d > 128) return 0;
+  // one row of partial sums per block and tensor, whichever kernel runs
+  const unsigned long long rows = static_cast<unsigned long long>(B) * H * N;
+  const size_t blocks = static_cast<size_t>(binattn::nr::blocks_for(rows, binattn::nr::kWarps));
+  return round256(2 * blocks * d * sizeof(float));
+}
+
+int binattn_norm_rope_backward(const void* q, const void* k, int dtype, const int64_t* strides, const void* dq_out,
+                               const void* dk_out, int grad_dtype, const float* w_q, const float* w_k,
+                               const float* cos, const float* sin, int rot, int per_batch, int interleaved, float eps,
+                               int B, int H, int N, int d, void* dq, void* dk, const int64_t* grad_strides,
+                               float* dw_q, float* dw_k, void* workspace, size_t workspace_bytes, void* stream) {
+  namespace nr = binattn::nr;
+  nr::Params p;
+  if (int rc = nr_params(q, k, dtype, strides, w_q, w_k, cos, sin, rot, per_batch, eps, B, H, N, d, &p)) return rc;
+  BINATTN_CHECK_PTR(dq_out);
+  BINATTN_CHECK_PTR(dk_out);
+  if (grad_dtype != BINATTN_F32 && grad_dtype != BINATTN_BF16)
+    return fail(BINATTN_ERR_DTYPE, "grad_dtype %d is neither BINATTN_F32 nor BINATTN_BF16", grad_dtype);
+  if (!dq) return fail(BINATTN_ERR_NULL, "dq is NULL");
+  if (!dk) return fail(BINATTN_ERR_NULL, "dk is NULL");
+  const uintptr_t es = dtype == BINATTN_F32 ? 4 : 2, gs = grad_dtype == BINATTN_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(dq) % es || reinterpret_cast<uintptr_t>(dk) % es)
+    return fail(BINATTN_ERR_ALIGN, "dq or dk is not aligned to its element");
+  if ((dw_q && !aligned16(dw_q)) || (dw_k && !aligned16(dw_k)))
+    return fail(BINATTN_ERR_ALIGN, "dw_q or dw_k is not 16-byte aligned");
+  p.dz[0] = dq_out;
+  p.dz[1] = dk_out;
+  p.out[0] = dq;
+  p.out[1] = dk;
+  if (int rc = nr_strides(grad_strides, B, H, N, d, "dq or dk", p.ob, p.oh, p.on)) return rc;
+  for (int t = 0; t < 2; ++t)
+    if (!nr_disjoint(p.ob[t], p.oh[t], p.on[t], B, H, N, d))
+      return fail(BINATTN_ERR_ARG, "the strides of %s make its rows overlap", t ? "dk" : "dq");
+  if (dw_q || dw_k) {
+    BINATTN_CHECK_PTR(workspace);
+    const size_t need = binattn_norm_rope_backward_workspace_bytes(B, H, N, d);
+    if (workspace_bytes < need)
+      return fail(BINATTN_ERR_ARG, "workspace of %zu bytes is below the %zu this shape needs", workspace_bytes, need);
+    p.dwpart = static_cast<float*>(workspace);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool inter = interleaved != 0;
+  const bool vec = nr::vec_ok(p, static_cast<int>(es), static_cast<int>(gs), true);
+  int blocks;
+  if (dtype == BINATTN_F32)
+    blocks = grad_dtype == BINATTN_F32 ? nr::launch<float, float, nr::kOpBwd>(p, inter, vec, st)
+                                       : nr::launch<float, uint16_t, nr::kOpBwd>(p, inter, vec, st);
+  else
+    blocks = grad_dtype == BINATTN_F32 ? nr::launch<uint16_t, float, nr::kOpBwd>(p, inter, vec, st)
+                                       : nr::launch<uint16_t, uint16_t, nr::kOpBwd>(p, inter, vec, st);
+  if (int rc = launch_status("norm_rope_backward kernel")) return rc;
+  if (p.dwpart) {
+    nr::norm_rope_dw_kernel<<<2, 1024, 0, st>>>(p.dwpart, blocks, d, dw_q, dw_k);
+    return launch_status("norm_rope_dw_kernel");
+  }
   return ok();
 }
 

@@ -1,0 +1,479 @@
+// norm_rope.cuh — what stands between a block's Q/K projection and its
+// attention: the RMS norm of every head's query and key and the rotation of
+// their channel pairs by the token's position, in one pass over the
+// projection's output (any token, head and batch strides); the same pass ended
+// in sign bits and alpha, binattn_pack's output; and its gradient.
+//
+// Per row x (one token of one head, d channels), weight w and the token's
+// tables cos_p, sin_p, p < R / 2:
+//   r = 1 / sqrt(mean x^2 + eps),  y_c = r x_c w_c
+//   z_a = y_a cos_p - y_b sin_p,  z_b = y_a sin_p + y_b cos_p
+// for the pair (a, b) = (p, p + R / 2) or, interleaved, (2p, 2p + 1), and
+// z_c = y_c for c >= R. Its gradient, with dz = dLoss / dz:
+//   dy = dz turned back (sin -> -sin),  dw_c = sum over rows of dy_c r x_c
+//   g = dy w,  dx = r (g - r x mean(g r x)).
+// fp32 throughout; each result is rounded once, when it is stored.
+//
+// The pass is bound by memory, so the mapping keeps loads wide and consecutive:
+// d / 8 lanes share a row, each with two quads of 4 channels (8 bytes of bf16,
+// 16 of fp32) chosen so that both members of its four pairs are its own, and
+// 32 / (d / 8) rows share a warp. A lane's channels are the same in every row,
+// so w and the sums of dw stay in registers. One thread per row, as
+// pack_bf16_rows_kernel has it, would cost a strided view 32 cache lines per
+// load. Rows are numbered (batch, token, head) with the head fastest: the rows
+// a block works on share a few tokens' tables. Shapes outside d % 8 == 0,
+// R % 8 == 0 and 4-element alignment take one warp per row and scalar loads.
+#pragma once
+#include "common.cuh"
+
+namespace binattn {
+namespace nr {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// Both tensors (index 0: q, 1: k; blockIdx.y) of one call. Strides in elements.
+struct Params {
+  const void* x[2];
+  long long xb[2], xh[2], xn[2];
+  const float* w[2];  // null: ones
+  const float* cosv;
+  const float* sinv;
+  int R, per_batch;
+  float eps;
+  int B, H, N, d;
+  void* out[2];        // norm_rope: [B,H,N,d]; backward: dx, strided
+  long long ob[2], oh[2], on[2];
+  uint32_t* bits[2];   // pack
+  float* alpha[2];
+  const void* dz[2];   // backward: [B,H,N,d]
+  float* dwpart;       // backward: [2][blocks][d] partial sums, or null
+};
+
+constexpr int kOpOut = 0, kOpPack = 1, kOpBwd = 2;
+
+__device__ __forceinline__ float ldf(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float ldf(const uint16_t* p) { return bf16_bits_to_float(__ldg(p)); }
+__device__ __forceinline__ void stf(float* p, float v) { *p = v; }
+__device__ __forceinline__ void stf(uint16_t* p, float v) { *p = float_to_bf16_bits(v); }
+
+// Four channels at once.
+__device__ __forceinline__ void ld4(const float* p, float (&f)[4]) {
+  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+__device__ __forceinline__ void ld4(const uint16_t* p, float (&f)[4]) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+  f[0] = __uint_as_float(v.x << 16);
+  f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(v.y << 16);
+  f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void st4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void st4(uint16_t* p, float a, float b, float c, float d) {
+  uint2 v;
+  v.x = float_to_bf16_bits(a) | static_cast<uint32_t>(float_to_bf16_bits(b)) << 16;
+  v.y = float_to_bf16_bits(c) | static_cast<uint32_t>(float_to_bf16_bits(d)) << 16;
+  *reinterpret_cast<uint2*>(p) = v;
+}
+
+// Whether p1 - p2 >= 0 for p1 = xa wa c and p2 = xb wb s (the sign of z, since
+// r > 0), exactly. t is their fp32 difference, off by at most 2^-23 (|p1| +
+// |p2|) and 2^-24 |t| from the two or three roundings, so its sign is right
+// beyond 1e-6 (|p1| + |p2|) (and above the range where products underflow);
+// closer to zero the products are taken in 64 bits, in one fixed order, so that
+// equal products cancel to an exact zero.
+__device__ __forceinline__ bool nonneg(float t, float p1, float p2, float xa, float wa, float c, float xb, float wb,
+                                       float s) {
+  if (fabsf(t) > 1e-6f * (fabsf(p1) + fabsf(p2)) && fabsf(t) > 1e-30f) return t > 0.f;
+  const double a = __dmul_rn(__dmul_rn(static_cast<double>(xa), static_cast<double>(wa)), static_cast<double>(c));
+  const double b = __dmul_rn(__dmul_rn(static_cast<double>(xb), static_cast<double>(wb)), static_cast<double>(s));
+  return __dsub_rn(a, b) >= 0.0;
+}
+
+// The token of row i (batch, token, head with the head fastest).
+struct Row {
+  int b, h, n;
+};
+__device__ __forceinline__ Row row_of(unsigned long long i, int H, int N, bool small) {
+  Row w;
+  unsigned tk;  // batch * N + token < 2^32
+  if (small) {
+    const unsigned u = static_cast<unsigned>(i);
+    tk = u / static_cast<unsigned>(H);
+    w.h = static_cast<int>(u - tk * static_cast<unsigned>(H));
+  } else {
+    tk = static_cast<unsigned>(i / static_cast<unsigned>(H));
+    w.h = static_cast<int>(i % static_cast<unsigned>(H));
+  }
+  w.b = static_cast<int>(tk / static_cast<unsigned>(N));
+  w.n = static_cast<int>(tk - static_cast<unsigned>(w.b) * static_cast<unsigned>(N));
+  return w;
+}
+
+// Sum over the c lanes of this lane's row (pos: its place in the row, base: the
+// row's first lane), to all of them, in a fixed order.
+__device__ __forceinline__ float row_sum(float v, int c, int pos, int base, bool pow2) {
+  if (pow2) {
+    for (int o = 1; o < c; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  for (int o = 1; o < c; o <<= 1) {
+    const float u = __shfl_down_sync(0xffffffffu, v, o);
+    if (pos + o < c) v += u;
+  }
+  return __shfl_sync(0xffffffffu, v, base);
+}
+
+// T: x's type, G: dz's (backward). kInter: pairs (2p, 2p + 1).
+template <typename T, typename G, int kOp, bool kInter>
+__global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p) {
+  constexpr int kU = 2;  // rows in flight per lane group
+  const int t = blockIdx.y;
+  const int d = p.d, H = p.H, N = p.N, half = p.R / 2;
+  const int c = d / 8, rpw = 32 / c;  // lanes per row, rows per warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = lane / c, pos = lane - grp * c, base = grp * c;
+  const bool pow2 = (c & (c - 1)) == 0;
+  const bool live = grp < rpw;  // lanes past the last whole row idle
+  const bool turns = pos < p.R / 8;
+  // this lane's two quads: the pairs' first and second members (or, interleaved
+  // or not rotated, eight consecutive channels)
+  const int ca = (kInter || !turns) ? 8 * pos : 4 * pos;
+  const int cb = (kInter || !turns) ? 8 * pos + 4 : half + 4 * pos;
+  const T* x = static_cast<const T*>(p.x[t]);
+  // first and second members of the lane's four pairs from its two quads, and back
+  auto split = [&](const float (&qa)[4], const float (&qb)[4], float (&f)[4], float (&s)[4]) {
+    if (kInter) {
+      f[0] = qa[0]; s[0] = qa[1]; f[1] = qa[2]; s[1] = qa[3];
+      f[2] = qb[0]; s[2] = qb[1]; f[3] = qb[2]; s[3] = qb[3];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = qa[i], s[i] = qb[i];
+    }
+  };
+  float wf[4] = {1.f, 1.f, 1.f, 1.f}, ws[4] = {1.f, 1.f, 1.f, 1.f};
+  if (p.w[t] && live) {
+    float qa[4], qb[4];
+    ld4(p.w[t] + ca, qa);
+    ld4(p.w[t] + cb, qb);
+    split(qa, qb, wf, ws);
+  }
+  float dwf[4] = {0.f, 0.f, 0.f, 0.f}, dws[4] = {0.f, 0.f, 0.f, 0.f};
+
+  const unsigned long long rows = static_cast<unsigned long long>(p.B) * H * N;
+  const bool small = rows <= 0xffffffffull;
+  const float inv_d = 1.f / static_cast<float>(d);
+  const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * kWarps * rpw * kU;
+  for (unsigned long long i0 = (static_cast<unsigned long long>(blockIdx.x) * kWarps + warp) * rpw * kU; i0 < rows;
+       i0 += step) {  // the trip count is warp-uniform
+    float xf[kU][4], xs[kU][4], cs[kU][4], sn[kU][4], zf[kU][4], zs[kU][4];
+    Row w[kU];
+    bool in[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const unsigned long long i = i0 + static_cast<unsigned>(u * rpw + grp);
+      in[u] = live && i < rows;
+      w[u] = row_of(in[u] ? i : 0, H, N, small);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) xf[u][e] = xs[u][e] = zf[u][e] = zs[u][e] = sn[u][e] = 0.f, cs[u][e] = 1.f;
+      if (in[u]) {
+        float qa[4], qb[4];
+        const T* src = x + w[u].b * p.xb[t] + w[u].h * p.xh[t] + w[u].n * p.xn[t];
+        ld4(src + ca, qa);
+        ld4(src + cb, qb);
+        split(qa, qb, xf[u], xs[u]);
+        if (turns) {
+          const size_t tok = (p.per_batch ? static_cast<size_t>(w[u].b) * N : 0) + w[u].n;
+          ld4(p.cosv + tok * half + 4 * pos, cs[u]);
+          ld4(p.sinv + tok * half + 4 * pos, sn[u]);
+        }
+        if constexpr (kOp == kOpBwd) {
+          const G* g = static_cast<const G*>(p.dz[t]) + ((static_cast<size_t>(w[u].b) * H + w[u].h) * N + w[u].n) * d;
+          ld4(g + ca, qa);
+          ld4(g + cb, qb);
+          split(qa, qb, zf[u], zs[u]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ss = fmaf(xf[u][e], xf[u][e], fmaf(xs[u][e], xs[u][e], ss));
+      const float r = rsqrtf(row_sum(ss, c, pos, base, pow2) * inv_d + p.eps);
+      if constexpr (kOp == kOpBwd) {
+        float gf[4], gs[4], dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float yf = zf[u][e] * cs[u][e] + zs[u][e] * sn[u][e];
+          const float ys = zs[u][e] * cs[u][e] - zf[u][e] * sn[u][e];
+          const float hf = xf[u][e] * r, hs = xs[u][e] * r;
+          dwf[e] = fmaf(yf, hf, dwf[e]);
+          dws[e] = fmaf(ys, hs, dws[e]);
+          gf[e] = yf * wf[e];
+          gs[e] = ys * ws[e];
+          dot = fmaf(gf[e], hf, fmaf(gs[e], hs, dot));
+        }
+        const float mean = row_sum(dot, c, pos, base, pow2) * inv_d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          zf[u][e] = r * (gf[e] - xf[u][e] * r * mean);
+          zs[u][e] = r * (gs[e] - xs[u][e] * r * mean);
+        }
+      }
+      if constexpr (kOp == kOpPack) {
+        float sum = 0.f;
+        uint32_t bf = 0, bs = 0;  // sign bits of the four pairs' members
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float uf = xf[u][e] * wf[e], us = xs[u][e] * ws[e];
+          const float p1 = uf * cs[u][e], p2 = us * sn[u][e], p3 = us * cs[u][e], p4 = -(uf * sn[u][e]);
+          const float tf = p1 - p2, ts = p3 - p4;
+          sum += fabsf(tf) + fabsf(ts);
+          bf |= (nonneg(tf, p1, p2, xf[u][e], wf[e], cs[u][e], xs[u][e], ws[e], sn[u][e]) ? 1u : 0u) << e;
+          bs |= (nonneg(ts, p3, p4, xs[u][e], ws[e], cs[u][e], xf[u][e], wf[e], -sn[u][e]) ? 1u : 0u) << e;
+        }
+        const float alpha = row_sum(sum, c, pos, base, pow2) * r * inv_d;
+        // byte pos of the row's sign words: channels 8 pos .. 8 pos + 7
+        uint32_t byte;
+        if (kInter) {
+          byte = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) byte |= ((bf >> e) & 1u) << (2 * e) | ((bs >> e) & 1u) << (2 * e + 1);
+        } else {
+          // quad q of the row is half a byte, held by lane src(q): the lower
+          // half of that lane's pair of nibbles, or the upper
+          const uint32_t mine = bf | bs << 4;
+          const int R8 = p.R / 8;
+          auto src = [&](int q, int& upper) {
+            const bool first = q < R8, second = !first && q < 2 * R8;
+            upper = first ? 0 : second ? 1 : (q & 1);
+            return base + (first ? q : second ? q - R8 : q / 2);
+          };
+          int u0, u1;
+          const int l0 = src(2 * pos, u0), l1 = src(2 * pos + 1, u1);
+          const uint32_t lo = __shfl_sync(0xffffffffu, mine, l0), hi = __shfl_sync(0xffffffffu, mine, l1);
+          byte = ((lo >> (4 * u0)) & 0xFu) | ((hi >> (4 * u1)) & 0xFu) << 4;
+        }
+        if (in[u]) {
+          const size_t row = (static_cast<size_t>(w[u].b) * H + w[u].h) * N + w[u].n;
+          const int wb = 4 * words_for(d);  // bytes per row, the last ones padding
+          uint8_t* dst = reinterpret_cast<uint8_t*>(p.bits[t]) + row * wb;
+          dst[pos] = static_cast<uint8_t>(byte);
+          if (pos == 0) {
+            for (int k = c; k < wb; ++k) dst[k] = 0;
+            p.alpha[t][row] = alpha;
+          }
+        }
+      } else {
+        if constexpr (kOp == kOpOut) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float yf = xf[u][e] * r * wf[e], ys = xs[u][e] * r * ws[e];
+            zf[u][e] = yf * cs[u][e] - ys * sn[u][e];
+            zs[u][e] = yf * sn[u][e] + ys * cs[u][e];
+          }
+        }
+        if (in[u]) {
+          T* dst = static_cast<T*>(p.out[t]) + w[u].b * p.ob[t] + w[u].h * p.oh[t] + w[u].n * p.on[t];
+          const float(&f)[4] = zf[u];
+          const float(&s)[4] = zs[u];
+          if (kInter) {
+            st4(dst + ca, f[0], s[0], f[1], s[1]);
+            st4(dst + cb, f[2], s[2], f[3], s[3]);
+          } else {
+            st4(dst + ca, f[0], f[1], f[2], f[3]);
+            st4(dst + cb, s[0], s[1], s[2], s[3]);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (kOp == kOpBwd) {
+    // the block's sums of dw: every lane group's registers, added in group order
+    if (!p.dwpart) return;
+    __shared__ float red[kThreads * 8];  // [group][d]: at most kThreads / c groups of 8 c channels
+    if (live) {
+      float* mine = red + (warp * rpw + grp) * d;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        mine[kInter ? 8 * pos + 2 * e : ca + e] = dwf[e];
+        mine[kInter ? 8 * pos + 2 * e + 1 : cb + e] = dws[e];
+      }
+    }
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < d; ch += kThreads) {
+      float s = 0.f;
+      for (int g = 0; g < kWarps * rpw; ++g) s += red[g * d + ch];
+      p.dwpart[(static_cast<size_t>(t) * gridDim.x + blockIdx.x) * d + ch] = s;
+    }
+  }
+}
+
+// Any d <= 128, R and alignment: one warp per row, lane l has channels l + 32 i.
+template <typename T, typename G, int kOp>
+__global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const Params p, int inter) {
+  const int t = blockIdx.y;
+  const int d = p.d, H = p.H, N = p.N, R = p.R, half = p.R / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* x = static_cast<const T*>(p.x[t]);
+  const float* wt = p.w[t];
+  const unsigned long long rows = static_cast<unsigned long long>(p.B) * H * N;
+  const bool small = rows <= 0xffffffffull;
+  const float inv_d = 1.f / static_cast<float>(d);
+  float dw[4] = {0.f, 0.f, 0.f, 0.f};
+  auto all_sum = [](float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  for (unsigned long long i = static_cast<unsigned long long>(blockIdx.x) * kWarps + warp; i < rows;
+       i += static_cast<unsigned long long>(gridDim.x) * kWarps) {
+    const Row w = row_of(i, H, N, small);
+    const T* src = x + w.b * p.xb[t] + w.h * p.xh[t] + w.n * p.xn[t];
+    const size_t row = (static_cast<size_t>(w.b) * H + w.h) * N + w.n;
+    const size_t tok = (p.per_batch ? static_cast<size_t>(w.b) * N : 0) + w.n;
+    const G* gz = kOp == kOpBwd ? static_cast<const G*>(p.dz[t]) + row * d : nullptr;
+    float xv[4], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ch = lane + 32 * k;
+      xv[k] = ch < d ? ldf(src + ch) : 0.f;
+      ss = fmaf(xv[k], xv[k], ss);
+    }
+    const float r = rsqrtf(all_sum(ss) * inv_d + p.eps);
+    float z[4] = {0.f, 0.f, 0.f, 0.f}, g[4] = {0.f, 0.f, 0.f, 0.f}, acc = 0.f;
+    uint32_t word = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ch = lane + 32 * k;
+      bool on = false;
+      if (ch < d) {
+        const float wc = wt ? __ldg(wt + ch) : 1.f;
+        // the pair partner, and the angle with the sign this member takes it in:
+        // z_c = y_c cos - y_partner sgn
+        int pc = ch;
+        float cs = 1.f, sg = 0.f;
+        if (ch < R) {
+          const bool first = inter ? !(ch & 1) : ch < half;
+          const int pr = inter ? ch >> 1 : first ? ch : ch - half;
+          pc = inter ? ch ^ 1 : first ? ch + half : ch - half;
+          cs = __ldg(p.cosv + tok * half + pr);
+          sg = __ldg(p.sinv + tok * half + pr);
+          if (!first) sg = -sg;
+        }
+        if constexpr (kOp == kOpBwd) {
+          // turned back: dy_c = dz_c cos + dz_partner sgn
+          const float dy = ldf(gz + ch) * cs + ldf(gz + pc) * sg;
+          const float xh = xv[k] * r;
+          dw[k] = fmaf(dy, xh, dw[k]);
+          g[k] = dy * wc;
+          acc = fmaf(g[k], xh, acc);
+        } else {
+          const float xp = ldf(src + pc), wp = wt ? __ldg(wt + pc) : 1.f;
+          const float p1 = xv[k] * wc * cs, p2 = xp * wp * sg;
+          const float tv = p1 - p2;
+          if constexpr (kOp == kOpPack) {
+            acc += fabsf(tv);
+            on = nonneg(tv, p1, p2, xv[k], wc, cs, xp, wp, sg);
+          } else {
+            z[k] = tv * r;
+          }
+        }
+      }
+      if constexpr (kOp == kOpPack) {
+        const uint32_t b = __ballot_sync(0xffffffffu, on);
+        if (lane == k) word = b;
+      }
+    }
+    if constexpr (kOp == kOpPack) {
+      const float alpha = all_sum(acc) * r * inv_d;
+      const int W = words_for(d);
+      if (lane < W) p.bits[t][row * W + lane] = word;
+      if (lane == 0) p.alpha[t][row] = alpha;
+    } else {
+      if constexpr (kOp == kOpBwd) {
+        const float mean = all_sum(acc) * inv_d;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = r * (g[k] - xv[k] * r * mean);
+      }
+      T* dst = static_cast<T*>(p.out[t]) + w.b * p.ob[t] + w.h * p.oh[t] + w.n * p.on[t];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (lane + 32 * k < d) stf(dst + lane + 32 * k, z[k]);
+    }
+  }
+  if constexpr (kOp == kOpBwd) {
+    if (!p.dwpart) return;
+    __shared__ float red[kWarps][128];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) red[warp][lane + 32 * k] = dw[k];
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < d; ch += kThreads) {
+      float s = 0.f;
+      for (int g = 0; g < kWarps; ++g) s += red[g][ch];
+      p.dwpart[(static_cast<size_t>(t) * gridDim.x + blockIdx.x) * d + ch] = s;
+    }
+  }
+}
+
+// dw of q (block 0) and k (block 1) from the blocks' partial sums: 8 slices of
+// the blocks per channel, each added in order, then the slices in order.
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, int blocks, int d,
+                                                            float* dwq, float* dwk) {
+  __shared__ float red[8][128];
+  const int ch = threadIdx.x & 127, slice = threadIdx.x >> 7;
+  const float* src = part + static_cast<size_t>(blockIdx.x) * blocks * d;
+  float s = 0.f;
+  if (ch < d)
+    for (int b = slice; b < blocks; b += 8) s += __ldg(src + static_cast<size_t>(b) * d + ch);
+  red[slice][ch] = s;
+  __syncthreads();
+  float* out = blockIdx.x ? dwk : dwq;
+  if (slice == 0 && ch < d && out) {
+    for (int g = 1; g < 8; ++g) s += red[g][ch];
+    out[ch] = s;
+  }
+}
+
+// Blocks per tensor of a launch: each warp's rows at least twice over before a
+// second round of blocks, at most 3 blocks per SM of a 148-SM part and tensor
+// (the kernels stride over the rest; the backward writes one row of partial
+// sums per block).
+constexpr int kMaxBlocks = 148 * 3;
+inline int blocks_for(unsigned long long rows, int rows_per_block) {
+  const unsigned long long b = (rows + rows_per_block - 1) / rows_per_block;
+  return b < kMaxBlocks ? static_cast<int>(b) : kMaxBlocks;
+}
+
+// Whether the vector kernel takes the call: see the head of this file.
+inline bool vec_ok(const Params& p, int es, int gs, bool bwd) {
+  if (p.d % 8 || p.R % 8) return false;
+  for (int t = 0; t < 2; ++t) {
+    if (reinterpret_cast<uintptr_t>(p.x[t]) % (4 * es) || p.xb[t] % 4 || p.xh[t] % 4 || p.xn[t] % 4) return false;
+    if (p.out[t] && (reinterpret_cast<uintptr_t>(p.out[t]) % (4 * es) || p.ob[t] % 4 || p.oh[t] % 4 || p.on[t] % 4))
+      return false;
+    if (bwd && reinterpret_cast<uintptr_t>(p.dz[t]) % (4 * gs)) return false;
+  }
+  return true;
+}
+
+template <typename T, typename G, int kOp>
+inline int launch(const Params& p, bool inter, bool vec, cudaStream_t st) {
+  const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.H * p.N;
+  if (vec) {
+    const int blocks = blocks_for(rows, kWarps * (32 / (p.d / 8)) * 2);
+    if (inter) norm_rope_rows_kernel<T, G, kOp, true><<<dim3(blocks, 2), kThreads, 0, st>>>(p);
+    else norm_rope_rows_kernel<T, G, kOp, false><<<dim3(blocks, 2), kThreads, 0, st>>>(p);
+    return blocks;
+  }
+  const int blocks = blocks_for(rows, kWarps);
+  norm_rope_any_kernel<T, G, kOp><<<dim3(blocks, 2), kThreads, 0, st>>>(p, inter);
+  return blocks;
+}
+
+}  // namespace nr
+}  // namespace binattn

@@ -409,6 +409,97 @@ int binattn_backward(const uint32_t *q_bits, const uint32_t *k_bits,
                      void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * binattn_norm_rope — the per-head RMS norm of queries and keys and the
+ * rotation of their channel pairs by position, in one pass over both.
+ *
+ * For every row x of d channels (one token of one head of q or of k), with the
+ * tensor's weight w (NULL: ones) and the token's tables cos_p, sin_p:
+ *   y_c = x_c w_c / sqrt(mean_c x_c^2 + eps)
+ *   z_a = y_a cos_p - y_b sin_p,  z_b = y_a sin_p + y_b cos_p
+ * for p < rot / 2, where (a, b) is (p, p + rot / 2), or (2p, 2p + 1) with
+ * interleaved != 0; z_c = y_c for c >= rot. fp32 inside, one rounding to the
+ * output's type.
+ *
+ *   q, k       [B, H, N, d] of `dtype`, device, aligned to the element (not to
+ *              16 bytes): the rows are contiguous, and `strides` (host, 6
+ *              numbers in elements: batch, head and token stride of q, then of
+ *              k; NULL: contiguous) places them, so that views of a fused
+ *              projection's output [B, N, 3, H, d] go in as they are. A stride
+ *              may be 0 (a broadcast input), not negative.
+ *   w_q, w_k   [d] fp32 or NULL, device.
+ *   cos, sin   [N, rot / 2] fp32, device, or [B, N, rot / 2] with per_batch
+ *              != 0 (each batch entry has positions of its own); a token that
+ *              is not rotated (a class token) has cos 1 and sin 0. NULL only
+ *              when rot is 0. Any axes' angles go in this table: binattn
+ *              applies it and does not compute it.
+ *   rot        channels that are rotated, even, 0 <= rot <= d.
+ *   eps        positive.
+ *   q_out, k_out  [B, H, N, d] of `dtype`, contiguous, device, written; must
+ *              not overlap an input or each other.
+ * Any d in 1..128. d % 8 == 0 and rot % 8 == 0 with addresses and strides of q
+ * and k in multiples of 4 elements run at memory speed; other calls take scalar loads.
+ * Errors: as binattn_pack; BINATTN_ERR_SHAPE for rot, BINATTN_ERR_ARG for eps
+ * and strides.
+ * Source: not in the pages; what current ViT/DiT blocks put between the
+ * projection and the attention whose Q and K the pages binarise (§2).
+ */
+int binattn_norm_rope(const void *q, const void *k, int dtype, const int64_t *strides,
+                      const float *w_q, const float *w_k, const float *cos, const float *sin,
+                      int rot, int per_batch, int interleaved, float eps,
+                      int B, int H, int N, int d, void *q_out, void *k_out, void *stream);
+
+/*
+ * binattn_norm_rope_pack — binattn_norm_rope ended in binattn_pack's output:
+ * bits and alpha of the unrounded z of q and of k, in one pass, with no z
+ * written. A bit is 1 exactly when x_a w_a cos - x_b w_b sin >= 0 (and
+ * likewise for the pair's second member), decided in 64-bit products where 32
+ * bits cannot tell; alpha = mean |z|, summed in fp32. (binattn_norm_rope
+ * followed by binattn_pack takes alpha from the rounded z.)
+ *   q_bits, k_bits    [B, H, N, W] uint32, alpha_q, alpha_k [B, H, N] fp32,
+ *                     device, written, as binattn_pack's.
+ * Other arguments and errors as binattn_norm_rope.
+ * Source: §2 scaled binary representations.
+ */
+int binattn_norm_rope_pack(const void *q, const void *k, int dtype, const int64_t *strides,
+                           const float *w_q, const float *w_k, const float *cos, const float *sin,
+                           int rot, int per_batch, int interleaved, float eps,
+                           int B, int H, int N, int d, uint32_t *q_bits, float *alpha_q,
+                           uint32_t *k_bits, float *alpha_k, void *stream);
+
+/*
+ * binattn_norm_rope_backward — the gradients of binattn_norm_rope for upstream
+ * gradients of z (and, with the straight-through estimator, of
+ * binattn_norm_rope_pack for the ds and dt of the binary backward):
+ * with dy = dz turned back by the same angles, r = 1 / sqrt(mean x^2 + eps)
+ * and g = dy w:  dx = r (g - x r mean(g x r)),  dw_c = sum over rows of
+ * dy_c x_c r.
+ *   q, k, dtype, strides, w_q, w_k, cos, sin, rot, per_batch, interleaved, eps
+ *                    as the forward had them.
+ *   dq_out, dk_out   [B, H, N, d] of `grad_dtype` (BINATTN_F32 or BF16, q's
+ *                    type or the other), contiguous, device: dLoss/dz.
+ *   dq, dk           [B, H, N, d] of `dtype`, device, aligned to the element,
+ *                    written, placed by grad_strides as q and k are by strides
+ *                    (so they can be views of the projection's gradient);
+ *                    their rows must not overlap each other.
+ *   dw_q, dw_k       [d] fp32, device, written; NULL skips one. The sums run
+ *                    in a fixed order: the same call gives the same bits.
+ *   workspace        device, 16-byte aligned, at least
+ *                    binattn_norm_rope_backward_workspace_bytes(...) bytes
+ *                    (the blocks' sums of dw), overwritten; may be NULL when
+ *                    both dw are.
+ * Errors as binattn_norm_rope; BINATTN_ERR_ARG for overlapping rows of dq or
+ * dk and for a workspace that is too small.
+ */
+size_t binattn_norm_rope_backward_workspace_bytes(int B, int H, int N, int d);
+int binattn_norm_rope_backward(const void *q, const void *k, int dtype, const int64_t *strides,
+                               const void *dq_out, const void *dk_out, int grad_dtype,
+                               const float *w_q, const float *w_k, const float *cos,
+                               const float *sin, int rot, int per_batch, int interleaved,
+                               float eps, int B, int H, int N, int d, void *dq, void *dk,
+                               const int64_t *grad_strides, float *dw_q, float *dw_k,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * binattn_scores_debug — writes the integer scores S [B, H, N, N] (int32,
  * device) that engine `engine` computes inside the forward pass, using the same
  * kernel and score routine. For testing only: it materialises the N x N matrix.
