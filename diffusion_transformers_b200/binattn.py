@@ -34,6 +34,8 @@ EXPORTS = (
     "binattn_ref_bf16_forward_workspace_bytes", "binattn_ref_bf16_forward_ws",
     "binattn_forward_sample_bias_workspace_bytes", "binattn_forward_sample_bias_ws",
     "binattn_backward_workspace_bytes", "binattn_backward",
+    "binattn_backward_bf16_workspace_bytes", "binattn_backward_bf16",
+    "binattn_ref_bf16_backward_workspace_bytes", "binattn_ref_bf16_backward",
     "binattn_norm_rope", "binattn_norm_rope_pack",
     "binattn_norm_rope_backward_workspace_bytes", "binattn_norm_rope_backward",
 )
@@ -83,6 +85,13 @@ def lib() -> ctypes.CDLL:
     L.binattn_backward_workspace_bytes.restype = ctypes.c_size_t
     L.binattn_backward.argtypes = [P, P, P, P, P, P, P, F, I, I, I, I, P, P, P, P, P, ctypes.c_size_t, P]
     L.binattn_backward.restype = I
+    for name in ("binattn_backward_bf16_workspace_bytes", "binattn_ref_bf16_backward_workspace_bytes"):
+        getattr(L, name).argtypes = [I, I, I, I, I, I]
+        getattr(L, name).restype = ctypes.c_size_t
+    L.binattn_backward_bf16.argtypes = [P, P, P, P, P, P, P, F, I, I, I, I, P, P, P, P, P, ctypes.c_size_t, P]
+    L.binattn_backward_bf16.restype = I
+    L.binattn_ref_bf16_backward.argtypes = [P, P, P, P, P, F, I, I, I, I, P, P, P, P, P, ctypes.c_size_t, P]
+    L.binattn_ref_bf16_backward.restype = I
     L.binattn_norm_rope.argtypes = [P, P, I, P, P, P, P, P, I, I, I, F, I, I, I, I, P, P, P]
     L.binattn_norm_rope.restype = I
     L.binattn_norm_rope_pack.argtypes = [P, P, I, P, P, P, P, P, I, I, I, F, I, I, I, I, P, P, P, P, P]
@@ -380,6 +389,65 @@ def backward(q_bits: torch.Tensor, k_bits: torch.Tensor, alpha_q: torch.Tensor, 
                                       _ptr(dbias), _ptr(workspace), ctypes.c_size_t(size), _stream(stream, dev)),
                "binattn_backward")
     return dV, ds, dt, dbias
+
+
+def _backward_buffers(shape, dev, with_dbias, need, workspace, stream):
+    """Three bf16 gradients, dbias (or None) and the workspace of a tensor-core backward."""
+    B, H, N, d = shape
+    with _on(stream, dev):
+        grads = [torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(3)]
+        dbias = torch.empty((H, N, N), dtype=torch.bfloat16, device=dev) if with_dbias else None
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    return grads, dbias, workspace, ctypes.c_size_t(workspace.numel() * workspace.element_size())
+
+
+def backward_bf16(q_bits: torch.Tensor, k_bits: torch.Tensor, alpha_q: torch.Tensor, alpha_k: torch.Tensor,
+                  bias: torch.Tensor | None, v: torch.Tensor, dO: torch.Tensor, softmax_scale: float,
+                  with_dbias: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """backward on the tensor cores: (dV, ds, dt, dbias) in bf16. Needs d % 8 == 0;
+    a bias may hold -inf (binattn_backward_bf16). workspace: uint8 CUDA tensor of at
+    least backward_bf16_workspace_bytes(...) bytes, allocated here when None."""
+    B, H, N, d = v.shape
+    _expect(dO, "dO", (B, H, N, d), (torch.bfloat16,))
+    dev = _forward_args(q_bits, k_bits, alpha_q, alpha_k, bias, v, None)
+    _device(dO, v, workspace)
+    need = backward_bf16_workspace_bytes(B, H, N, d, bias is not None, with_dbias)
+    with torch.cuda.device(dev):
+        (dV, ds, dt), dbias, workspace, size = _backward_buffers((B, H, N, d), dev, with_dbias, need, workspace, stream)
+        _check(lib().binattn_backward_bf16(_ptr(q_bits), _ptr(k_bits), _ptr(alpha_q), _ptr(alpha_k), _ptr(bias), _ptr(v),
+                                           _ptr(dO), float(softmax_scale), B, H, N, d, _ptr(dV), _ptr(ds), _ptr(dt),
+                                           _ptr(dbias), _ptr(workspace), size, _stream(stream, dev)),
+               "binattn_backward_bf16")
+    return dV, ds, dt, dbias
+
+
+def backward_bf16_workspace_bytes(B: int, H: int, N: int, d: int, has_bias: bool, with_dbias: bool) -> int:
+    return int(lib().binattn_backward_bf16_workspace_bytes(B, H, N, d, int(bool(has_bias)), int(bool(with_dbias))))
+
+
+def ref_bf16_backward(q: torch.Tensor, k: torch.Tensor, bias: torch.Tensor | None, v: torch.Tensor, dO: torch.Tensor,
+                      softmax_scale: float, with_dbias: bool = True, workspace: torch.Tensor | None = None,
+                      stream=None):
+    """Gradients of ref_bf16_forward for an upstream gradient dO (bf16 [B,H,N,d]):
+    (dq, dk, dv, dbias) in bf16, dbias [H,N,N] summed over the batch, or None without
+    with_dbias. The probabilities are computed again from q and k."""
+    B, H, N, d = q.shape
+    for name, t in (("q", q), ("k", k), ("v", v), ("dO", dO)):
+        _expect(t, name, (B, H, N, d), (torch.bfloat16,))
+    _expect(bias, "bias", (H, N, N), (torch.bfloat16,))
+    dev = _device(q, k, bias, v, dO, workspace)
+    need = ref_bf16_backward_workspace_bytes(B, H, N, d, bias is not None, with_dbias)
+    with torch.cuda.device(dev):
+        (dq, dk, dv), dbias, workspace, size = _backward_buffers((B, H, N, d), dev, with_dbias, need, workspace, stream)
+        _check(lib().binattn_ref_bf16_backward(_ptr(q), _ptr(k), _ptr(bias), _ptr(v), _ptr(dO), float(softmax_scale), B, H,
+                                               N, d, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(workspace), size,
+                                               _stream(stream, dev)), "binattn_ref_bf16_backward")
+    return dq, dk, dv, dbias
+
+
+def ref_bf16_backward_workspace_bytes(B: int, H: int, N: int, d: int, has_bias: bool, with_dbias: bool) -> int:
+    return int(lib().binattn_ref_bf16_backward_workspace_bytes(B, H, N, d, int(bool(has_bias)), int(bool(with_dbias))))
 
 
 def rope_tables(positions: torch.Tensor, rot: int, theta: float = 10000.0):

@@ -18,6 +18,7 @@
 #include "quantv.cuh"
 #include "bwd_simt.cuh"
 #include "norm_rope.cuh"
+#include "bwd_tc.cuh"
 
 namespace {
 
@@ -879,6 +880,80 @@ int binattn_norm_rope_backward(const void* q, const void* k, int dtype, const in
     nr::norm_rope_dw_kernel<<<2, 1024, 0, st>>>(p.dwpart, blocks, d, dw_q, dw_k);
     return launch_status("norm_rope_dw_kernel");
   }
+  return ok();
+}
+
+namespace {
+// What the two tensor-core backwards check alike.
+int check_backward_tc(const uint16_t* bias, const uint16_t* v, const uint16_t* dO, float softmax_scale, int B, int H,
+                      int N, int d, const uint16_t* dbias, size_t need, void* workspace, size_t workspace_bytes) {
+  BINATTN_CHECK_PTR(v);
+  BINATTN_CHECK_PTR(dO);
+  if (bias && !aligned16(bias)) return fail(BINATTN_ERR_ALIGN, "bias is not 16-byte aligned");
+  if (dbias && !aligned16(dbias)) return fail(BINATTN_ERR_ALIGN, "dbias is not 16-byte aligned");
+  if (!std::isfinite(softmax_scale)) return fail(BINATTN_ERR_ARG, "softmax_scale is not finite");
+  if (int rc = check_shape(B, H, N, d)) return rc;
+  if (d % 8 != 0)
+    return fail(BINATTN_ERR_UNSUPPORTED, "the tensor-core backward needs d %% 8 == 0 (d = %d)", d);
+  BINATTN_CHECK_PTR(workspace);
+  if (workspace_bytes < need)
+    return fail(BINATTN_ERR_ARG, "workspace of %zu bytes is below the %zu this shape needs", workspace_bytes, need);
+  return BINATTN_OK;
+}
+size_t backward_tc_bytes(int B, int H, int N, int d, bool bin, bool bias, bool dbias) {
+  if (B < 1 || H < 1 || N < 1 || d < 1 || d > 128 || d % 8 || static_cast<long long>(B) * H > 65535 || N > 65535)
+    return 0;
+  return binattn::bt::workspace(B, H, N, d, bin, bias, dbias).total;
+}
+}  // namespace
+
+size_t binattn_ref_bf16_backward_workspace_bytes(int B, int H, int N, int d, int has_bias, int with_dbias) {
+  return backward_tc_bytes(B, H, N, d, false, has_bias != 0, with_dbias != 0);
+}
+
+int binattn_ref_bf16_backward(const uint16_t* q, const uint16_t* k, const uint16_t* bias, const uint16_t* v,
+                              const uint16_t* dO, float softmax_scale, int B, int H, int N, int d, uint16_t* dq,
+                              uint16_t* dk, uint16_t* dv, uint16_t* dbias, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  BINATTN_CHECK_PTR(q);
+  BINATTN_CHECK_PTR(k);
+  BINATTN_CHECK_PTR(dq);
+  BINATTN_CHECK_PTR(dk);
+  BINATTN_CHECK_PTR(dv);
+  const size_t need = binattn_ref_bf16_backward_workspace_bytes(B, H, N, d, bias != nullptr, dbias != nullptr);
+  if (int rc = check_backward_tc(bias, v, dO, softmax_scale, B, H, N, d, dbias, need, workspace, workspace_bytes))
+    return rc;
+  std::string msg;
+  if (int rc = binattn::bt::backward(q, k, nullptr, nullptr, nullptr, nullptr, bias, v, dO, softmax_scale, B, H, N, d,
+                                     dq, dk, dv, dbias, static_cast<char*>(workspace),
+                                     static_cast<cudaStream_t>(stream), &msg))
+    return fail(rc, "%s", msg.c_str());
+  return ok();
+}
+
+size_t binattn_backward_bf16_workspace_bytes(int B, int H, int N, int d, int has_bias, int with_dbias) {
+  return backward_tc_bytes(B, H, N, d, true, has_bias != 0, with_dbias != 0);
+}
+
+int binattn_backward_bf16(const uint32_t* q_bits, const uint32_t* k_bits, const float* alpha_q, const float* alpha_k,
+                          const uint16_t* bias, const uint16_t* v, const uint16_t* dO, float softmax_scale, int B,
+                          int H, int N, int d, uint16_t* dV, uint16_t* ds, uint16_t* dt, uint16_t* dbias,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  BINATTN_CHECK_PTR(q_bits);
+  BINATTN_CHECK_PTR(k_bits);
+  BINATTN_CHECK_PTR(alpha_q);
+  BINATTN_CHECK_PTR(alpha_k);
+  BINATTN_CHECK_PTR(dV);
+  BINATTN_CHECK_PTR(ds);
+  BINATTN_CHECK_PTR(dt);
+  const size_t need = binattn_backward_bf16_workspace_bytes(B, H, N, d, bias != nullptr, dbias != nullptr);
+  if (int rc = check_backward_tc(bias, v, dO, softmax_scale, B, H, N, d, dbias, need, workspace, workspace_bytes))
+    return rc;
+  std::string msg;
+  if (int rc = binattn::bt::backward(nullptr, nullptr, q_bits, k_bits, alpha_q, alpha_k, bias, v, dO, softmax_scale,
+                                     B, H, N, d, ds, dt, dV, dbias, static_cast<char*>(workspace),
+                                     static_cast<cudaStream_t>(stream), &msg))
+    return fail(rc, "%s", msg.c_str());
   return ok();
 }
 

@@ -409,6 +409,66 @@ int binattn_backward(const uint32_t *q_bits, const uint32_t *k_bits,
                      void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * binattn_backward_bf16 — binattn_backward on the tensor cores, with its
+ * gradients in bf16: the same dV, ds, dt and dbias (see there), for training
+ * steps. P and dlogit (times the other side's alpha) are rounded to bf16 before
+ * their products, which accumulate in fp32; the softmax statistics, D and the
+ * sum over b stay in fp32; every gradient is rounded once.
+ *   q_bits ... dO   as binattn_backward. The bias may hold -inf (a mask): such
+ *                   a pair has no weight, and a query whose row holds nothing
+ *                   else passes no gradient on. With rows of the type's lowest
+ *                   value instead the weights are uniform, as in the formula.
+ *   dV, ds, dt      bf16 [B, H, N, d], device, written.
+ *   dbias           bf16 [H, N, N], device, written, or NULL.
+ *   workspace       device, 16-byte aligned, at least
+ *                   binattn_backward_bf16_workspace_bytes(...) bytes: the row
+ *                   log-sum-exp and D; the sign words as bf16 +-1 and the
+ *                   padded alphas; with N % 8 != 0 a padded copy of the bias;
+ *                   and for dbias over more batch entries than one pass sums
+ *                   (2 for d > 80, 3 for d > 64, else 4) fp32 sums of
+ *                   H * N * N, several times over where H * N is small.
+ *                   Overwritten; nothing in it needs to start at zero. Two
+ *                   calls that may overlap (other streams, two captured graphs)
+ *                   need two workspaces.
+ * Needs d % 8 == 0 (BINATTN_ERR_UNSUPPORTED otherwise: binattn_backward takes
+ * any d). The same call gives the same bits: every sum has one order.
+ * Errors as binattn_backward.
+ */
+size_t binattn_backward_bf16_workspace_bytes(int B, int H, int N, int d, int has_bias,
+                                             int with_dbias);
+int binattn_backward_bf16(const uint32_t *q_bits, const uint32_t *k_bits,
+                          const float *alpha_q, const float *alpha_k,
+                          const uint16_t *bias, const uint16_t *v, const uint16_t *dO,
+                          float softmax_scale, int B, int H, int N, int d, uint16_t *dV,
+                          uint16_t *ds, uint16_t *dt, uint16_t *dbias, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * binattn_ref_bf16_backward — the gradients of binattn_ref_bf16_forward's
+ * result for an upstream gradient dO, on the same kernels: with c =
+ * softmax_scale, logit = c <q_i, k_j> + bias and P, dP, D, dlogit as in
+ * binattn_backward,
+ *   dq_i = c sum_j dlogit_ij k_j,  dk_j = c sum_i dlogit_ij q_i,
+ *   dv_j = sum_i P_ij dO_i,  dbias = sum_b dlogit.
+ *   q, k, bias, v   as binattn_ref_bf16_forward (a bias may hold -inf, as
+ *                   above); dO bf16 [B, H, N, d], device.
+ *   dq, dk, dv      bf16 [B, H, N, d], device, written.
+ *   dbias           bf16 [H, N, N], device, written, or NULL.
+ *   workspace       device, 16-byte aligned, at least
+ *                   binattn_ref_bf16_backward_workspace_bytes(...) bytes.
+ * P is computed again from q and k, so neither the forward's output nor its
+ * statistics are needed. Needs d % 8 == 0. Rounding, workspace and errors as
+ * binattn_backward_bf16.
+ */
+size_t binattn_ref_bf16_backward_workspace_bytes(int B, int H, int N, int d, int has_bias,
+                                                 int with_dbias);
+int binattn_ref_bf16_backward(const uint16_t *q, const uint16_t *k, const uint16_t *bias,
+                              const uint16_t *v, const uint16_t *dO, float softmax_scale,
+                              int B, int H, int N, int d, uint16_t *dq, uint16_t *dk,
+                              uint16_t *dv, uint16_t *dbias, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
  * binattn_norm_rope — the per-head RMS norm of queries and keys and the
  * rotation of their channel pairs by position, in one pass over both.
  *
