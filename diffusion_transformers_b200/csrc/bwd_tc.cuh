@@ -20,17 +20,21 @@
 // call gives the same bits. The price against one kernel that adds dQ with
 // atomics is two more score products and exps.
 //
-// The three share one machine. The streamed operand (K and V, or Q and dO) comes
-// in tiles of 64 rows by TMA into a ring of stages, as 64-channel panels of
-// 128-byte swizzled rows: one panel serves both as the K-major operand of the
-// score products and as the MN-major operand of the gradient products. The
-// kept operand (128 rows) sits in tensor memory. Scores and dP of a tile are
-// two 128 x 64 fp32 accumulators in one of two tensor-memory buffers; P or dL
-// goes back as bf16 over its own half of the scores. 16 compute warps: eight
-// per buffer (tiles alternate), four per 32-column half, one thread per row.
-// LSE and D are known before any exp of the second pass, so threads need
-// nothing of one another inside a tile. Warp 16 issues the MMAs, warp 17 the
-// copies. Bounded waits as in fwd_tc2.cuh.
+// The three share one machine. tile_kernel first lays q, k, v and dO (binary: the
+// signs of q and k as +-1) out as the tensor cores take them: tiles of 64 rows,
+// each a block of 8-channel groups, [group][row][8]. Such a block serves both as
+// the K-major operand of the score products and as the MN-major operand of the
+// gradient products, needs no padding of the head dim beyond 16, and comes into
+// a ring of stages as one contiguous copy: tensor-map boxes of 144-byte rows
+// (d = 72) took the copy engine 1100 cycles a tile, more than the arithmetic. The
+// kept operand (128 rows) sits in tensor memory. Scores and dP of a tile are two
+// 128 x 64 fp32 accumulators in one of two tensor-memory buffers, and each of
+// two compute warpgroups (one thread per kept row) has a buffer of its own and
+// takes every second tile. P or dL goes back as bf16, over the scores or dP or
+// (rows_kernel, where they fit) into one of three slots. LSE and D are known
+// before any exp of the second pass, so threads need nothing of one another
+// inside a tile. Warps 8 and 10 issue the MMAs, warp 9 the copies. Bounded waits
+// as in fwd_tc2.cuh.
 //
 // Rounding: P, dL (binary: dL times the alpha of the summed side) and the
 // results to bf16, half a step each; all else fp32.
@@ -39,6 +43,7 @@
 #include <atomic>
 #include <cstring>
 #include <string>
+#include <type_traits>
 
 #include "fwd_tc.cuh"
 #include "fwd_tc2.cuh"
@@ -53,26 +58,31 @@ using tc2::named_sync;
 
 constexpr int kRows = 128;               // kept rows per CTA (MMA M, TMEM lanes)
 constexpr int kCols = 64;                // streamed rows per tile (score MMA N)
-constexpr int kComputeWarps = 16;
-constexpr int kMmaWarp = 16, kTmaWarp = 17;
-constexpr int kThreads = 18 * 32;
+constexpr int kComputeWarps = 8;         // one warpgroup per buffer, one thread per kept row
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kGradWarp = 10;
+constexpr int kThreads = 11 * 32;
 constexpr int kCompute = kComputeWarps * 32;
-constexpr int kPanel = kCols * 128;      // bytes: 64 rows x 64 channels bf16
+constexpr int kGroup = kCols * 16;       // bytes of a tile's 8-channel group
+constexpr int kBiasPanel = 64 * 128;     // bytes of a box of 64 rows x 64 keys of the bias
 constexpr int kBiasBytes = kRows * kCols * 2;
 constexpr int kVecBytes = 1024;          // per stage: up to four vectors of 64 floats
 constexpr int kBar = 1;                  // named barrier of the compute warps
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Params {
-  const uint16_t* a0;  // kept operands [B,H,N,d]: q and dO (rows, dbias), k and v (cols)
+  const uint16_t* a0;  // kept operands, tiled: q and dO (rows, dbias), k and v (cols)
   const uint16_t* a1;
+  const uint16_t* b0;  // streamed operands, tiled: k and v (rows, dbias), q and dO (cols)
+  const uint16_t* b1;
   const float* aq;     // binary: c alpha_q (times log2 e without a bias), padded [BH][Npad]
   const float* ak;     // binary: alpha_k, padded [BH][Npad]
   float cs;            // bf16: factor of the scores (times log2 e without a bias)
   float out;           // factor of dQ (rows) or dK (cols)
-  float* lse;          // [BH][Npad]: what logits are taken relative to (see exp2v)
-  float* l2;           // [BH][Npad]: with a bias, log2 of the row's sum
-  float* D;            // [BH][Npad]
+  // Row vectors, [BH][Npad], all negated: what logits are taken relative to (see
+  // exp2v), with a bias log2 of the row's sum, and D.
+  float* nlse;
+  float* nl2;
+  float* nD;
   uint16_t* g0;        // rows: dQ; cols: dV; dbias: dbias
   uint16_t* g1;        // cols: dK
   float* part;         // dbias: fp32 partial sums [nsplit][H][N][N]
@@ -80,48 +90,86 @@ struct Params {
   int nb, nchunks, nsplit, jsplit;  // dbias
 };
 
-// Operand descriptor of 128-byte swizzled rows (8-row groups sbo = 1024 bytes
-// apart; MN-major: 64-element panels lbo apart).
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Descriptors of operands in 8 x 16-byte blocks without a swizzle: lbo and sbo
+// are the distances of blocks in the leading and the other direction.
+__device__ __forceinline__ uint64_t make_desc(uint32_t lo, uint32_t sbo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((sbo >> 4) | (1u << 14)));
+  return d;
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
-// D[128 x 64] = A[128 x ch16 * 16] B[64 x ...]^T: A in tensor memory (bf16
-// pairs, 8 columns per 16 channels) or shared memory (128-row panels), B a
-// 64-row tile.
-template <bool kSS>
-__device__ __forceinline__ void issue_scores(uint32_t d_col, uint32_t a, uint32_t b, int ch16) {
+// D[128 x 64] = A[128 x 16 kCh] B[64 x 16 kCh]^T: A in tensor memory (bf16
+// pairs, 8 columns per 16 channels) or shared memory ([group][128 rows][8]), B
+// a tile. The channel count is a template argument: with a loop around them,
+// the products issue at half the rate of the tensor cores.
+template <bool kSS, int kCh>
+__device__ __forceinline__ void issue_scores(uint32_t d_col, uint32_t a, uint32_t b, uint32_t lead) {
   constexpr uint32_t id = idesc_bf16(kRows, kCols, false);
+  const uint32_t bl = desc_lo(b, kGroup), al = desc_lo(a, 2 * kGroup);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (k >= ch16) break;
-    const uint64_t bd = desc_sw128(b + (k >> 2) * kPanel + (k & 3) * 32, 16);
-    if constexpr (kSS) mma_ss_warp(d_col, desc_sw128(a + (k >> 2) * 2 * kPanel + (k & 3) * 32, 16), bd, id, k > 0);
-    else mma_ts_warp(d_col, a + k * 8, bd, id, k > 0);
+  for (int k = 0; k < kCh; ++k) {
+    const uint64_t bd = make_desc(bl + k * (2 * kGroup >> 4), 128);
+    if constexpr (kSS) mma_ss_lead(d_col, make_desc(al + k * (4 * kGroup >> 4), 128), bd, id, k > 0, lead);
+    else mma_ts_lead(d_col, a + k * 8, bd, id, k > 0, lead);
   }
 }
-// D[128 x DP] += A[128 x 64] B[64 x DP]: A bf16 pairs in tensor memory, its two
-// 32-column halves 32 columns apart; B a 64-row tile, channels along N.
-__device__ __forceinline__ void issue_grad(uint32_t d_col, uint32_t a, uint32_t b, uint32_t id, bool accumulate) {
+// D[128 x 16 kCh] += A[128 x 64] B[64 x 16 kCh]: A bf16 pairs in tensor memory,
+// its two 32-row halves `gap` columns apart; B a tile, channels along N.
+template <int kCh>
+__device__ __forceinline__ void issue_grad(uint32_t d_col, uint32_t a, int gap, uint32_t b, bool accumulate,
+                                           uint32_t lead) {
+  constexpr uint32_t id = idesc_bf16(kRows, 16 * kCh, true);
+  const uint32_t bl = desc_lo(b, 128);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    mma_ts_warp(d_col, a + (k >> 1) * 32 + (k & 1) * 8, desc_sw128(b + k * 2048, kPanel), id, accumulate || k > 0);
+    mma_ts_lead(d_col, a + (k >> 1) * gap + (k & 1) * 8, make_desc(bl + k * 16, kGroup), id, accumulate || k > 0, lead);
+}
+// f<kCh>() for the channel count of a call.
+template <class F>
+__device__ __forceinline__ bool with_channels(int ch16, F f) {
+  switch (ch16) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 5: return f(std::integral_constant<int, 5>());
+    case 6: return f(std::integral_constant<int, 6>());
+    case 7: return f(std::integral_constant<int, 7>());
+    default: return f(std::integral_constant<int, 8>());
+  }
 }
 
-// Thread r's row of a kept operand into its TMEM lane as bf16 pairs, channels
-// >= d and rows that are not valid as zeros.
-__device__ __forceinline__ void stage_row(const uint16_t* row, bool valid, int d, int DP, uint32_t col) {
-  for (int c = 0; c < DP; c += 16) {
-    uint32_t w[8];
+// Row `row` of a tiled operand: its 16-byte group g is at [g * kCols].
+__device__ __forceinline__ const uint4* tiled_row(const uint16_t* t, int bh, int nt, int row, int DP) {
+  return reinterpret_cast<const uint4*>(t) + (static_cast<size_t>(bh) * nt + row / kCols) * (DP / 8) * kCols + row % kCols;
+}
+// A thread's row of a kept operand, all of its loads under way at once, and from
+// there into its TMEM lane as bf16 pairs or into shared memory; a row that is not
+// valid is zeros.
+struct KeptRow {
+  uint4 v[16];
+};
+__device__ __forceinline__ void load_row(KeptRow& k, const uint4* row, bool valid, int DP) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (valid && c + 8 * e < d) v = __ldg(reinterpret_cast<const uint4*>(row + c + 8 * e));
-      w[4 * e] = v.x; w[4 * e + 1] = v.y; w[4 * e + 2] = v.z; w[4 * e + 3] = v.w;
+  for (int g = 0; g < 16; ++g) k.v[g] = valid && g < DP / 8 ? __ldg(row + g * kCols) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void stage_row(const KeptRow& k, int DP, uint32_t col) {
+#pragma unroll
+  for (int g = 0; g < 16; g += 2) {
+    if (g < DP / 8) {
+      const uint32_t w[8] = {k.v[g].x,     k.v[g].y,     k.v[g].z,     k.v[g].w,
+                             k.v[g + 1].x, k.v[g + 1].y, k.v[g + 1].z, k.v[g + 1].w};
+      tmem_st8(col + 4 * g, w);
     }
-    tmem_st8(col + c / 2, w);
   }
+}
+__device__ __forceinline__ void stage_row_smem(const KeptRow& k, int DP, uint8_t* dst, int r) {
+#pragma unroll
+  for (int g = 0; g < 16; ++g)
+    if (g < DP / 8) *reinterpret_cast<uint4*>(dst + g * 2 * kGroup + r * 16) = k.v[g];
 }
 
 // 32 TMEM columns of fp32 times f, as bf16, to row[c0 .. c0 + 32) below d.
@@ -147,6 +195,16 @@ __device__ __forceinline__ float2 widen(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// Row r's bias columns of half h of a tile (half of a 128-byte swizzled row of
+// the stage's box) as packed pairs.
+__device__ __forceinline__ void load_bias(const uint8_t* box, int r, int h, uint32_t (&b)[16]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint4 v = *reinterpret_cast<const uint4*>(box + r * 128 + (((4 * h + u) ^ (r & 7)) << 4));
+    b[4 * u] = v.x; b[4 * u + 1] = v.y; b[4 * u + 2] = v.z; b[4 * u + 3] = v.w;
+  }
+}
+
 // Logits of kN columns in place. Without a bias they are in log2 units (the
 // factor log2 e is in ci), with one in natural units, so that a bias of the
 // type's lowest value does not overflow. bias: the thread's columns as packed
@@ -167,66 +225,102 @@ __device__ __forceinline__ void logits(uint32_t* s, const float* ak, float ci, c
       x[e + u] = kBias ? __ffma2_rn(x[e + u], c2, widen(bias[e + u])) : __fmul2_rn(x[e + u], c2);
   }
 }
+// 2^y of two values (y <= 1 or so) without the special-function unit: y = n + f
+// with n the nearest integer (added to 1.5 * 2^23 it stands in the low bits of
+// the sum), 2^f by a polynomial fitted to the smallest relative error on [-1/2,
+// 1/2] with constant term 1 (9.2e-8, in fp32 1.6e-7: no worse than ex2.approx),
+// and n added to the exponent. y is cut off at -127, where f is 0 and the
+// result's bits are all 0: masked pairs keep a weight of exactly 0.
+__device__ __forceinline__ float2 ex2_fma(float2 y) {
+  y = make_float2(fmaxf(y.x, -127.f), fmaxf(y.y, -127.f));
+  const float2 t = __fadd2_rn(y, make_float2(12582912.f, 12582912.f));
+  const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), y);
+  float2 p = make_float2(0.00132647272f, 0.00132647272f);
+  p = __ffma2_rn(p, f, make_float2(0.00967151269f, 0.00967151269f));
+  p = __ffma2_rn(p, f, make_float2(0.0555073374f, 0.0555073374f));
+  p = __ffma2_rn(p, f, make_float2(0.240222421f, 0.240222421f));
+  p = __ffma2_rn(p, f, make_float2(0.693146978f, 0.693146978f));
+  p = __ffma2_rn(p, f, make_float2(1.f, 1.f));
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
 // exp of x minus `top`, x in the units of logits(). Without a bias, top is the
 // max or the log-sum-exp. With one, a row may consist of masked logits of
 // -1e9 or the type's lowest value, where max + log(sum) would lose the sum: top
 // is the max, and the (log2 of the) sum is taken off after the subtraction, in
 // the multiply-add that changes the units.
-template <bool kBias>
+// kFma takes it on the FMA pipe (below).
+template <bool kBias, bool kFma = false>
 __device__ __forceinline__ float2 exp2v(float2 x, float2 minus_top, float2 minus_l2 = make_float2(0.f, 0.f)) {
   float2 y = __fadd2_rn(x, minus_top);
   if constexpr (kBias) y = __ffma2_rn(y, make_float2(kLog2e, kLog2e), minus_l2);
+  if constexpr (kFma) return ex2_fma(y);
   return make_float2(ex2(y.x), ex2(y.y));
 }
+// Every kFmaEvery-th pair of a row's exps runs on the FMA pipe, which the
+// kernels leave half idle, where the special-function unit sets their pace.
+constexpr int kFmaEvery = 4;
+__device__ __forceinline__ constexpr bool on_fma(int pair) { return pair % kFmaEvery == kFmaEvery - 1; }
 
 // Shared memory: the stages, then (cols, kSS) the kept operands, then scratch.
 struct Map {
-  int tile, vec, stage, kept, scratch, bars, bytes;
+  int tile, vec, stage, stages, kept, scratch, bars, bytes;
 };
-__host__ __device__ inline Map smem_map(int d, bool bias, int stages, bool kept, int scratch) {
+constexpr int kMaxSmem = 227 * 1024;
+constexpr int kMaxStages = 8;
+constexpr int kBarBytes = 512;
+__host__ __device__ inline Map smem_map(int d, bool bias, bool kept, int scratch) {
   Map m;
-  const int np = d > 64 ? 2 : 1;
-  m.tile = np * kPanel;                                // one streamed matrix
+  m.tile = (d + 15) / 16 * 16 * 128;                   // one streamed matrix
   m.vec = 2 * m.tile + (bias ? kBiasBytes : 0);        // vectors, after both and the bias
   m.stage = m.vec + kVecBytes;
-  m.kept = stages * m.stage;
+  // As many stages as fit: a tile holds its stage until its gradient products
+  // are done, some 2500 cycles, and the next copy takes 1000 more.
+  const int room = (kMaxSmem - kBarBytes - scratch - (kept ? 4 * m.tile : 0)) / m.stage;
+  m.stages = room < kMaxStages ? room : kMaxStages;
+  m.kept = m.stages * m.stage;
   m.scratch = m.kept + (kept ? 4 * m.tile : 0);
   m.bars = m.scratch + scratch;
-  m.bytes = m.bars + 256;
+  m.bytes = m.bars + kBarBytes;
   return m;
 }
 constexpr int kMinSmem = 120 * 1024;  // one CTA per SM: each holds all of its tensor memory
 
 struct Bars {
-  uint64_t *full, *empty, *s_full, *p_full, *a_ready, *o_done, *kept, *drain;
+  uint64_t *full, *empty, *s_full, *p_full, *r_full, *g_done, *a_ready, *o_done, *drain;
   uint32_t* tmem;
   volatile int* abort;
   __device__ explicit Bars(uint8_t* p) {
     uint64_t* b = reinterpret_cast<uint64_t*>(p);
-    full = b;            // [4] a stage's copies landed
-    empty = b + 4;       // [4] every reader is done with the stage
-    s_full = b + 8;      // [2] scores and dP of the buffer's tile
-    p_full = b + 10;     // [2] the 256 threads of the buffer are done with it (and wrote P / dL)
-    a_ready = b + 12;    // kept operands staged, accumulators read (512 threads)
-    o_done = b + 13;     // the item's last MMA
-    kept = b + 14;       // kept operands in shared memory landed
-    drain = b + 15;
-    tmem = reinterpret_cast<uint32_t*>(b + 16);
-    abort = reinterpret_cast<volatile int*>(b + 17);
+    full = b;            // [8] a stage's copies landed
+    empty = b + 8;       // [8] every reader is done with the stage
+    p_full = b + 16;     // [8] tile g's 128 threads wrote its P / dL (g % 8: a tile is waited for
+                         // before the eighth one after it has a stage)
+    s_full = b + 24;     // [2] scores and dP of the buffer's tile
+    r_full = b + 26;     // [2] its 128 threads hold the tile's scores and dP in registers
+    g_done = b + 28;     // [3] the gradient products from a slot of dL
+    a_ready = b + 31;    // kept operands staged, accumulators read (256 threads)
+    o_done = b + 32;     // the item's last MMA
+    drain = b + 33;      // [2] an issuing warp's last MMA
+    tmem = reinterpret_cast<uint32_t*>(b + 35);
+    abort = reinterpret_cast<volatile int*>(b + 36);
   }
   __device__ void init() {
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
+      mbar_init(&p_full[i], kCompute / 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kCompute / 2);
+      mbar_init(&r_full[i], kCompute / 2);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(&g_done[i], 1);
     mbar_init(a_ready, kCompute);
     mbar_init(o_done, 1);
-    mbar_init(kept, 1);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -237,10 +331,36 @@ struct Bars {
 // the ten score products of a tile issue in 390 cycles instead of 665).
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
 
-// A bounded wait of a whole warp, with one answer.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+// A bounded wait of a whole warp, with one answer; of one barrier, or of two at
+// once. What runs when a barrier is not complete yet stays out of line: the
+// issuing warp passes through several waits per tile and is slowed by what it
+// has to fetch.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_slow(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, volatile int* abort) {
+  const bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1);
+  if (__all_sync(0xffffffffu, r0 && r1)) return true;
+  return wait_slow(b0, p0, abort) && wait_slow(b1, p1, abort);
+}
+
+// A place in the ring of stages: the slot, and the parity of its round.
+struct Ring {
+  int n, s;
+  uint32_t ph = 0;
+  __device__ Ring(int stages, int first) : n(stages), s(first) {}
+  __device__ void step(int k) {
+    s += k;
+    if (s >= n) {
+      s -= n;
+      ph ^= 1;
+    }
+  }
+};
 
 // Common start and end of the kernels.
 __device__ __forceinline__ uint32_t begin(Bars& b, int warp) {
@@ -265,35 +385,32 @@ __device__ __forceinline__ void end(uint32_t tmem, int warp) {
 // The copying thread's last act: its `issued` copies have all landed (bounded).
 __device__ __forceinline__ void settle(Bars& b, int issued, int stages) {
   volatile int never = 0;
-  for (int g = issued > stages ? issued - stages : 0; g < issued; ++g)
-    mbar_wait(&b.full[g % stages], (g / stages) & 1, &never);
+  for (int s = 0; s < stages && s < issued; ++s) mbar_wait(&b.full[s], ((issued - 1 - s) / stages) & 1, &never);
 }
-__device__ __forceinline__ void drain_mma(Bars& b) {
-  mma_commit_warp(b.drain);
+__device__ __forceinline__ void drain_mma(Bars& b, int which = 0) {
+  mma_commit_lead(&b.drain[which], elect_one());
   volatile int never = 0;
-  mbar_wait(b.drain, 0, &never);
+  mbar_wait(&b.drain[which], 0, &never);
 }
 
 // Tensor memory of rows_kernel and dbias_kernel; cols_kernel sets its own
 // accumulator columns.
 constexpr int kBuf = 128;         // columns per buffer: scores [0, 64), dP [64, 128)
 constexpr int kAcc = 256;
-constexpr int kRowsQ = 384, kRowsDO = 448;
-constexpr int kRowStages = 4;
-constexpr int kRowsScratch = 3 * 4 * kRows * 4;   // [m, l, sum][warpgroup][row] floats
+constexpr int kMaxTs = 80;        // widest head dim (rounded up to 16) whose operands leave room for slots
+constexpr int kRowsScratch = 3 * 2 * kRows * 4;   // [m, l, sum][warpgroup][row] floats
 constexpr int kDbiasScratch = 4 * 4 * kRows * 4;  // [LSE, D, factor, log2 sum][batch entry][row]
+constexpr int kDbiasOut = kComputeWarps * 2048;   // the warps' pieces of the result
 
 template <bool kBin, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
-rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-            const __grid_constant__ CUtensorMap tm_bias) {
+rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kS = kRowStages;
-  const Map mp = smem_map(p.d, kBias, kS, false, kRowsScratch);
+  const Map mp = smem_map(p.d, kBias, false, kRowsScratch);
   Bars bar(smem + mp.bars);
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const int N = p.N, d = p.d, DP = (d + 15) / 16 * 16, np = d > 64 ? 2 : 1;
-  const int nkt = (N + kCols - 1) / kCols, T = 2 * nkt;
+  const int N = p.N, d = p.d, DP = (d + 15) / 16 * 16, nt = (N + kCols - 1) / kCols;
+  const int nkt = nt, T = 2 * nkt;
   const int nit = (N + kRows - 1) / kRows;
   const int G = static_cast<int>(gridDim.x);
   const int n_items = (p.items - static_cast<int>(blockIdx.x) + G - 1) / G;
@@ -305,98 +422,111 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k, const __gr
     bh = b * p.H + h;
     i0 = qt * kRows;
   };
+  // tensor memory: buffers, dQ, Q and dO, then (where they fit) three slots of dL
+  const int q_col = kAcc + DP, do_col = q_col + DP / 2, p_col = do_col + DP / 2;
   const uint32_t tmem = begin(bar, warp);
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
       bool ok = true;
       int g = 0;
+      Ring at_ring(mp.stages, 0);
       const uint32_t bytes = 2u * mp.tile + (kBias ? kBiasBytes : 0) + (kBin ? kCols * 4 : 0);
       for (int it = 0; ok && it < n_items; ++it) {
         int bh, h, i0;
         item(it, bh, h, i0);
-        for (int t = 0; t < T; ++t, ++g) {
-          const int s = g % kS, j0 = (t < nkt ? t : t - nkt) * kCols;
-          if (g >= kS && !(ok = mbar_wait(&bar.empty[s], ((g / kS) - 1) & 1, bar.abort))) break;
+        for (int t = 0; t < T; ++t, ++g, at_ring.step(1)) {
+          const int s = at_ring.s, j0 = (t < nkt ? t : t - nkt) * kCols;
+          if (!(ok = mbar_wait(&bar.empty[s], at_ring.ph ^ 1, bar.abort))) break;  // at once in the first round
           uint8_t* st = smem + s * mp.stage;
           mbar_arrive_expect_tx(&bar.full[s], bytes);
-          for (int c = 0; c < np; ++c) {
-            tma_load_3d(st + c * kPanel, &tm_k, 64 * c, j0, bh, &bar.full[s]);
-            tma_load_3d(st + mp.tile + c * kPanel, &tm_v, 64 * c, j0, bh, &bar.full[s]);
-          }
+          const size_t at = (static_cast<size_t>(bh) * nt + j0 / kCols) * (mp.tile / 2);
+          bulk_load(st, p.b0 + at, mp.tile, &bar.full[s]);
+          bulk_load(st + mp.tile, p.b1 + at, mp.tile, &bar.full[s]);
           if constexpr (kBias) tma_load_3d(st + 2 * mp.tile, &tm_bias, j0, i0, h, &bar.full[s]);
           if constexpr (kBin)
             bulk_load(st + mp.vec, p.ak + static_cast<size_t>(bh) * p.Npad + j0, kCols * 4, &bar.full[s]);
         }
       }
-      settle(bar, g, kS);
+      settle(bar, g, mp.stages);
     }
-  } else if (warp == kMmaWarp) {
-    // the whole warp runs this (see mma_ts_warp)
-    const uint32_t id = idesc_bf16(kRows, DP, true);
-    bool ok = true;
-    for (int it = 0; ok && it < n_items; ++it) {
-      if (!(ok = wait_warp(bar.a_ready, it & 1, bar.abort))) break;
-      tc_fence_after();
-      for (int t = 0; t < T + 2; ++t) {
-        const int g = it * T + t, b = g & 1;
-        if (t >= 2) {  // the tile before last: its buffer is free, its dL written
-          if (!(ok = wait_warp(&bar.p_full[b], ((g - 2) >> 1) & 1, bar.abort))) break;
-          tc_fence_after();
-          const int s = (g - 2) % kS;
-          if (t - 2 >= nkt)
-            issue_grad(tmem + kAcc, tmem + b * kBuf, smem_u32(smem + s * mp.stage), id, t - 2 > nkt);
-          mma_commit_warp(&bar.empty[s]);
-        }
-        if (t < T) {
-          const int s = g % kS;
-          if (!(ok = wait_warp(&bar.full[s], (g / kS) & 1, bar.abort))) break;
-          const uint32_t st = smem_u32(smem + s * mp.stage);
-          issue_scores<false>(tmem + b * kBuf, tmem + kRowsQ, st, DP / 16);
-          issue_scores<false>(tmem + b * kBuf + 64, tmem + kRowsDO, st + mp.tile, DP / 16);
-          mma_commit_warp(&bar.s_full[b]);
+  } else if (warp == kMmaWarp || warp == kGradWarp) {
+    // Whole warps run this (see mma_ts_lead). One issues the scores and dP of a
+    // tile once its buffer is free (slots of dL: once the tile before is in
+    // registers; dL over the scores: once its dQ products are done) and its
+    // stage is full; the other a tile's dQ products once its dL is written,
+    // and frees the stage.
+    const uint32_t lead = elect_one();
+    with_channels(DP / 16, [&](auto ch) {
+      constexpr int kCh = decltype(ch)::value;
+      constexpr bool kSlots = kCh * 16 <= kMaxTs;
+      Ring ring(mp.stages, 0);
+      for (int it = 0, g = 0; it < n_items; ++it) {
+        if (warp == kMmaWarp) {
+          if (!wait_warp(bar.a_ready, it & 1, bar.abort)) return false;
+          for (int t = 0; t < T; ++t, ++g, ring.step(1)) {
+            const int b = g & 1, s = ring.s;
+            uint64_t* const full = &bar.full[s];
+            const uint32_t ph = ring.ph;
+            if (g < 2 ? !wait_warp(full, ph, bar.abort)
+                      : !wait_warp(full, ph, kSlots ? &bar.r_full[b] : &bar.g_done[b], ((g - 2) >> 1) & 1, bar.abort))
+              return false;
+            tc_fence_after();
+            const uint32_t st = smem_u32(smem + s * mp.stage);
+            issue_scores<false, kCh>(tmem + b * kBuf, tmem + q_col, st, lead);
+            issue_scores<false, kCh>(tmem + b * kBuf + 64, tmem + do_col, st + mp.tile, lead);
+            mma_commit_lead(&bar.s_full[b], lead);
+          }
+        } else {
+          for (int t = 0; t < T; ++t, ++g, ring.step(1)) {
+            const int b = g & 1, s = ring.s, slot = kSlots ? g % 3 : b;
+            if (!wait_warp(&bar.p_full[g & 7], (g >> 3) & 1, bar.abort)) return false;
+            tc_fence_after();
+            if (t >= nkt)
+              issue_grad<kCh>(tmem + kAcc, tmem + (kSlots ? p_col + slot * 32 : b * kBuf), kSlots ? 16 : 32,
+                              smem_u32(smem + s * mp.stage), t > nkt, lead);
+            mma_commit_lead(&bar.g_done[slot], lead);
+            mma_commit_lead(&bar.empty[s], lead);
+          }
+          mma_commit_lead(bar.o_done, lead);
         }
       }
-      if (ok) mma_commit_warp(bar.o_done);
-    }
-    drain_mma(bar);
+      return true;
+    });
+    drain_mma(bar, warp == kGradWarp);
   } else {
-    const int wg = warp >> 2, buf = wg >> 1, hh = wg & 1;
+    const int wg = warp >> 2;  // also this warpgroup's buffer
     const int r = ((warp & 3) << 5) | lane;
     const uint32_t lb = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_col = lb + buf * kBuf + 32 * hh, dp_col = s_col + 64;
-    float* sc = reinterpret_cast<float*>(smem + mp.scratch);  // [3][4 wg][128 rows]
+    const uint32_t s_col = lb + wg * kBuf, dp_col = s_col + 64;
+    float* sc = reinterpret_cast<float*>(smem + mp.scratch);  // [3][2 warpgroups][128 rows]
     bool ok = true;
-    auto wait_all = [&](uint64_t* b, uint32_t parity) { return wait_warp(b, parity, bar.abort); };
-    // scores, dP and the stage of tile g in registers, as logits; columns >= N
-    // are -inf
+    // Half h (32 columns) of the tile at j0: scores as logits (columns >= N as
+    // -inf) and dP.
     uint32_t xr[32], dp[32];
-    auto tile = [&](int g, int j0, float ci) -> const uint8_t* {
-      const int s = g % kS;
-      ok = ok && wait_all(&bar.s_full[buf], (g >> 1) & 1) && wait_all(&bar.full[s], (g / kS) & 1);
+    Ring ring(mp.stages, wg);  // this buffer's tiles are every second one
+    auto arrived = [&](int g) {
+      ok = ok && (kBias || kBin ? wait_warp(&bar.s_full[wg], (g >> 1) & 1, &bar.full[ring.s], ring.ph, bar.abort)
+                                : wait_warp(&bar.s_full[wg], (g >> 1) & 1, bar.abort));
       tc_fence_after();
-      const uint8_t* st = smem + s * mp.stage;
-      if (ok) {
-        tmem_ld32(s_col, xr);
-        tmem_ld32(dp_col, dp);
-        uint32_t bias[16];
-        if constexpr (kBias) {
-          const uint8_t* br = st + 2 * mp.tile + r * 128;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint4 v = *reinterpret_cast<const uint4*>(br + (((4 * hh + u) ^ (r & 7)) << 4));
-            bias[4 * u] = v.x; bias[4 * u + 1] = v.y; bias[4 * u + 2] = v.z; bias[4 * u + 3] = v.w;
-          }
-        }
-        tmem_ld_wait();
-        logits<kBin, kBias, 32>(xr, reinterpret_cast<const float*>(st + mp.vec) + 32 * hh, ci, bias);
-        if (j0 + kCols > N) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (j0 + 32 * hh + e >= N) xr[e] = 0xff800000u;
-        }
+    };
+    auto half = [&](int h, int j0, float ci) {
+      const uint8_t* st = smem + ring.s * mp.stage;
+      uint32_t bias[16];
+      tmem_ld32(s_col + 32 * h, xr);
+      tmem_ld32(dp_col + 32 * h, dp);
+      if constexpr (kBias) load_bias(st + 2 * mp.tile, r, h, bias);
+      tmem_ld_wait();
+      if (h == 1) {
+        tc_fence_before();
+        mbar_arrive(&bar.r_full[wg]);
       }
-      return st;
+      logits<kBin, kBias, 32>(xr, reinterpret_cast<const float*>(st + mp.vec) + 32 * h, ci, bias);
+      if (j0 + 32 * h + 32 > N) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (j0 + 32 * h + e >= N) xr[e] = 0xff800000u;
+      }
     };
     for (int it = 0; it < n_items; ++it) {
       int bh, h, i0;
@@ -404,94 +534,114 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k, const __gr
       const int row = i0 + r;
       const bool valid = row < N;
       const size_t tok = static_cast<size_t>(bh) * N + (valid ? row : 0);
-      if (ok && wg < 2) stage_row((wg ? p.a1 : p.a0) + tok * d, valid, d, DP, lb + (wg ? kRowsDO : kRowsQ));
+      if (ok) {
+        KeptRow kept;
+        load_row(kept, tiled_row(wg ? p.a1 : p.a0, bh, nt, valid ? row : 0, DP), valid, DP);
+        stage_row(kept, DP, lb + (wg ? do_col : q_col));
+      }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar.a_ready);
       const float ci = !kBin ? p.cs : valid ? p.aq[static_cast<size_t>(bh) * p.Npad + row] : 0.f;
       const int g0 = it * T;
 
-      // ---- first pass: m, l and sum exp(x - m) dP of this thread's columns
+      // ---- first pass: m, l and sum exp(x - m) dP of this warpgroup's tiles
       float m = -INFINITY, l = 0.f, aD = 0.f;
-      int t = buf;  // T is even, so a tile's buffer is its parity in the item
-      for (; t < nkt; t += 2) {
-        tile(g0 + t, t * kCols, ci);
+      int t = wg;  // T is even, so a tile's buffer is its parity in the item
+      for (; t < nkt; t += 2, ring.step(2)) {
+        arrived(g0 + t);
         if (!ok) continue;
-        tc_fence_before();
-        mbar_arrive(&bar.p_full[buf]);  // everything of the tile is in registers
-        float* x = reinterpret_cast<float*>(xr);
-        float a[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          a[k] = max3f(x[k], x[k + 4], x[k + 8]);
-          a[k] = max3f(a[k], x[k + 12], x[k + 16]);
-          a[k] = max3f(a[k], x[k + 20], x[k + 24]);
-          a[k] = fmaxf(a[k], x[k + 28]);
-        }
-        const float mn = fmaxf(m, fmaxf(max3f(a[0], a[1], a[2]), a[3]));
-        const float ms = mn == -INFINITY ? 0.f : mn;  // nothing but -inf so far: every exp is 0
-        const float corr = exp2v<kBias>(make_float2(m, m), make_float2(-ms, -ms)).x;
-        m = mn;
-        float2 l2 = make_float2(0.f, 0.f), d2 = l2;
-        const float2 nm = make_float2(-ms, -ms);
+        for (int hf = 0; hf < 2; ++hf) {
+          half(hf, t * kCols, ci);
+          if (hf == 1) mbar_arrive(&bar.p_full[(g0 + t) & 7]);
+          const float* x = reinterpret_cast<const float*>(xr);
+          float a[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 ex = exp2v<kBias>(reinterpret_cast<float2*>(xr)[e], nm);
-          l2 = __fadd2_rn(l2, ex);
-          d2 = __ffma2_rn(ex, reinterpret_cast<float2*>(dp)[e], d2);
+          for (int q = 0; q < 4; ++q) {
+            a[q] = max3f(x[q], x[q + 4], x[q + 8]);
+            a[q] = max3f(a[q], x[q + 12], x[q + 16]);
+            a[q] = max3f(a[q], x[q + 20], x[q + 24]);
+            a[q] = fmaxf(a[q], x[q + 28]);
+          }
+          const float mn = fmaxf(m, fmaxf(max3f(a[0], a[1], a[2]), a[3]));
+          const float ms = mn == -INFINITY ? 0.f : mn;  // nothing but -inf so far: every exp is 0
+          const float corr = exp2v<kBias>(make_float2(m, m), make_float2(-ms, -ms)).x;
+          m = mn;
+          float2 l2 = make_float2(0.f, 0.f), d2 = l2;
+          const float2 nm = make_float2(-ms, -ms);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 xe = reinterpret_cast<const float2*>(xr)[e];
+            const float2 ex = on_fma(e) ? exp2v<kBias, true>(xe, nm) : exp2v<kBias>(xe, nm);
+            l2 = __fadd2_rn(l2, ex);
+            d2 = __ffma2_rn(ex, reinterpret_cast<const float2*>(dp)[e], d2);
+          }
+          l = fmaf(l, corr, l2.x + l2.y);
+          aD = fmaf(aD, corr, d2.x + d2.y);
         }
-        l = fmaf(l, corr, l2.x + l2.y);
-        aD = fmaf(aD, corr, d2.x + d2.y);
       }
-      // ---- the row's four partial results (two buffers, two halves) joined
+      // ---- the row's two partial results (one per warpgroup) joined
       sc[wg * kRows + r] = m;
-      sc[(4 + wg) * kRows + r] = l;
-      sc[(8 + wg) * kRows + r] = aD;
+      sc[(2 + wg) * kRows + r] = l;
+      sc[(4 + wg) * kRows + r] = aD;
       named_sync(kBar, kCompute);
-      float M = -INFINITY, Ls = 0.f, Ds = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) M = fmaxf(M, sc[k * kRows + r]);
-      // a row with nothing but -inf: no weights, so +inf makes every P 0
-      float lse = INFINITY, l2 = 0.f, D = 0.f;
+      const float M = fmaxf(sc[r], sc[kRows + r]);
+      // a row with nothing but -inf: no weights, so -inf makes every P 0
+      float nlse = -INFINITY, nl2 = 0.f, nD = 0.f;
       if (M > -INFINITY) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float w = exp2v<kBias>(make_float2(sc[k * kRows + r], 0.f), make_float2(-M, -M)).x;
-          Ls = fmaf(w, sc[(4 + k) * kRows + r], Ls);
-          Ds = fmaf(w, sc[(8 + k) * kRows + r], Ds);
-        }
-        l2 = log2f(Ls);
-        lse = kBias ? M : M + l2;
-        D = Ds / Ls;
+        const float2 w = exp2v<kBias>(make_float2(sc[r], sc[kRows + r]), make_float2(-M, -M));
+        const float Ls = fmaf(w.x, sc[2 * kRows + r], w.y * sc[3 * kRows + r]);
+        const float Ds = fmaf(w.x, sc[4 * kRows + r], w.y * sc[5 * kRows + r]);
+        nl2 = -log2f(Ls);
+        nlse = kBias ? -M : nl2 - M;
+        nD = -(Ds / Ls);
       }
       if (wg == 0 && row < p.Npad) {
-        p.lse[static_cast<size_t>(bh) * p.Npad + row] = valid ? lse : INFINITY;
-        p.D[static_cast<size_t>(bh) * p.Npad + row] = valid ? D : 0.f;
-        if (kBias) p.l2[static_cast<size_t>(bh) * p.Npad + row] = valid ? l2 : 0.f;
+        const size_t at = static_cast<size_t>(bh) * p.Npad + row;
+        p.nlse[at] = valid ? nlse : -INFINITY;
+        p.nD[at] = valid ? nD : 0.f;
+        if (kBias) p.nl2[at] = valid ? nl2 : 0.f;
       }
-      // ---- second pass: dL (binary: times alpha_k) as bf16 over the scores
-      const float2 nl = make_float2(-lse, -lse), nl2 = make_float2(-l2, -l2), nD = make_float2(-D, -D);
-      for (; t < T; t += 2) {
-        const int j0 = (t - nkt) * kCols;
-        const uint8_t* st = tile(g0 + t, j0, ci);
+      // ---- second pass: dL (binary: times alpha_k) as bf16 into its slot, or
+      // over the scores
+      const float2 nlse2 = make_float2(nlse, nlse), nl22 = make_float2(nl2, nl2), nD2 = make_float2(nD, nD);
+      for (; t < T; t += 2, ring.step(2)) {
+        const int g = g0 + t;
+        arrived(g);
         if (!ok) continue;
-        const float* ak = reinterpret_cast<const float*>(st + mp.vec) + 32 * hh;
-        uint32_t pk[16];
+        const float* ak = reinterpret_cast<const float*>(smem + ring.s * mp.stage + mp.vec);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 P = exp2v<kBias>(reinterpret_cast<float2*>(xr)[e], nl, nl2);
-          float2 dl = __fmul2_rn(P, __fadd2_rn(reinterpret_cast<float2*>(dp)[e], nD));
-          if constexpr (kBin) dl = __fmul2_rn(dl, *reinterpret_cast<const float2*>(ak + 2 * e));
-          pk[e] = pack_bf16x2(dl.x, dl.y);
+        for (int hf = 0; hf < 2; ++hf) {
+          half(hf, (t - nkt) * kCols, ci);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 xe = reinterpret_cast<const float2*>(xr)[e];
+            const float2 P = on_fma(e) ? exp2v<kBias, true>(xe, nlse2, nl22) : exp2v<kBias>(xe, nlse2, nl22);
+            float2 dl = __fmul2_rn(P, __fadd2_rn(reinterpret_cast<const float2*>(dp)[e], nD2));
+            if constexpr (kBin) dl = __fmul2_rn(dl, *reinterpret_cast<const float2*>(ak + 32 * hf + 2 * e));
+            pk[e] = pack_bf16x2(dl.x, dl.y);
+          }
+          if (DP <= kMaxTs) {
+            // the slot's last dQ products, three tiles ago, are done with it
+            if (hf == 0 && g >= 3) {
+              if (!(ok = wait_warp(&bar.g_done[g % 3], (g / 3 - 1) & 1, bar.abort))) break;
+              tc_fence_after();
+            }
+            tmem_st16(lb + p_col + (g % 3) * 32 + 16 * hf, pk);
+          } else {
+            tmem_st16(s_col + 32 * hf, pk);
+          }
         }
-        tmem_st16(s_col, pk);
+        if (!ok) continue;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bar.p_full[buf]);
+        mbar_arrive(&bar.p_full[g & 7]);
       }
-      ok = ok && wait_all(bar.o_done, it & 1);
+      ok = ok && wait_warp(bar.o_done, it & 1, bar.abort);
       tc_fence_after();
-      if (ok && 32 * wg < d) store_row(lb + kAcc, p.out, p.g0 + tok * d, valid, 32 * wg, d);
+      for (int c0 = 32 * wg; ok && c0 < d; c0 += 64) store_row(lb + kAcc, p.out, p.g0 + tok * d, valid, c0, d);
     }
   }
   end(tmem, warp);
@@ -502,16 +652,13 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k, const __gr
 // columns + 3 DP > 512).
 template <bool kBin, bool kBias, bool kSS>
 __global__ void __launch_bounds__(kThreads, 1)
-cols_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-            const __grid_constant__ CUtensorMap tm_bias, const __grid_constant__ CUtensorMap tm_k,
-            const __grid_constant__ CUtensorMap tm_v) {
+cols_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kS = kSS ? 3 : 4;
-  const Map mp = smem_map(p.d, kBias, kS, kSS, 0);
+  const Map mp = smem_map(p.d, kBias, kSS, 0);
   Bars bar(smem + mp.bars);
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const int N = p.N, d = p.d, DP = (d + 15) / 16 * 16, np = d > 64 ? 2 : 1;
-  const int T = (N + kCols - 1) / kCols;
+  const int N = p.N, d = p.d, DP = (d + 15) / 16 * 16, nt = (N + kCols - 1) / kCols;
+  const int T = nt;
   const int njt = (N + kRows - 1) / kRows;
   const int G = static_cast<int>(gridDim.x);
   const int n_items = (p.items - static_cast<int>(blockIdx.x) + G - 1) / G;
@@ -528,158 +675,162 @@ cols_kernel(const Params p, const __grid_constant__ CUtensorMap tm_q, const __gr
   if (warp == kTmaWarp) {
     if (lane == 0) {
       bool ok = true;
-      int g = 0, kept = 0;  // copies of stages and of kept operands issued
+      int g = 0;
+      Ring at_ring(mp.stages, 0);
       const uint32_t bytes = 2u * mp.tile + (kBias ? kBiasBytes + kCols * 4 : 0) + (kBin ? 3 : 2) * kCols * 4;
       for (int it = 0; ok && it < n_items; ++it) {
         int bh, h, j0;
         item(it, bh, h, j0);
-        if constexpr (kSS) {
-          if (it > 0 && !(ok = mbar_wait(bar.o_done, (it - 1) & 1, bar.abort))) break;
-          ++kept;
-          mbar_arrive_expect_tx(bar.kept, 4u * mp.tile);
-          for (int c = 0; c < np; ++c)
-            for (int u = 0; u < 2; ++u) {
-              tma_load_3d(smem + mp.kept + (2 * c + u) * kPanel, &tm_k, 64 * c, j0 + 64 * u, bh, bar.kept);
-              tma_load_3d(smem + mp.kept + 2 * mp.tile + (2 * c + u) * kPanel, &tm_v, 64 * c, j0 + 64 * u, bh,
-                          bar.kept);
-            }
-        }
-        for (int t = 0; t < T; ++t, ++g) {
-          const int s = g % kS, i0 = t * kCols;
-          if (g >= kS && !(ok = mbar_wait(&bar.empty[s], ((g / kS) - 1) & 1, bar.abort))) break;
+        for (int t = 0; t < T; ++t, ++g, at_ring.step(1)) {
+          const int s = at_ring.s, i0 = t * kCols;
+          if (!(ok = mbar_wait(&bar.empty[s], at_ring.ph ^ 1, bar.abort))) break;  // at once in the first round
           uint8_t* st = smem + s * mp.stage;
           mbar_arrive_expect_tx(&bar.full[s], bytes);
-          for (int c = 0; c < np; ++c) {
-            tma_load_3d(st + c * kPanel, &tm_q, 64 * c, i0, bh, &bar.full[s]);
-            tma_load_3d(st + mp.tile + c * kPanel, &tm_do, 64 * c, i0, bh, &bar.full[s]);
-          }
+          const size_t tl = (static_cast<size_t>(bh) * nt + t) * (mp.tile / 2);
+          bulk_load(st, p.b0 + tl, mp.tile, &bar.full[s]);
+          bulk_load(st + mp.tile, p.b1 + tl, mp.tile, &bar.full[s]);
           if constexpr (kBias)
             for (int u = 0; u < 2; ++u)
-              tma_load_3d(st + 2 * mp.tile + u * kPanel, &tm_bias, j0 + 64 * u, i0, h, &bar.full[s]);
+              tma_load_3d(st + 2 * mp.tile + u * kBiasPanel, &tm_bias, j0 + 64 * u, i0, h, &bar.full[s]);
           const size_t at = static_cast<size_t>(bh) * p.Npad + i0;
-          bulk_load(st + mp.vec, p.lse + at, kCols * 4, &bar.full[s]);
-          bulk_load(st + mp.vec + 256, p.D + at, kCols * 4, &bar.full[s]);
+          bulk_load(st + mp.vec, p.nlse + at, kCols * 4, &bar.full[s]);
+          bulk_load(st + mp.vec + 256, p.nD + at, kCols * 4, &bar.full[s]);
           if constexpr (kBin) bulk_load(st + mp.vec + 512, p.aq + at, kCols * 4, &bar.full[s]);
-          if constexpr (kBias) bulk_load(st + mp.vec + 768, p.l2 + at, kCols * 4, &bar.full[s]);
+          if constexpr (kBias) bulk_load(st + mp.vec + 768, p.nl2 + at, kCols * 4, &bar.full[s]);
         }
       }
-      settle(bar, g, kS);
-      if (kept > 0) {
-        volatile int never = 0;
-        mbar_wait(bar.kept, (kept - 1) & 1, &never);
-      }
+      settle(bar, g, mp.stages);
     }
   } else if (warp == kMmaWarp) {
-    // the whole warp runs this (see mma_ts_warp)
-    const uint32_t id = idesc_bf16(kRows, DP, true);
-    bool ok = true;
-    for (int it = 0; ok && it < n_items; ++it) {
-      if (!(ok = wait_warp(bar.a_ready, it & 1, bar.abort))) break;
-      if (kSS && !(ok = wait_warp(bar.kept, it & 1, bar.abort))) break;
-      tc_fence_after();
-      for (int t = 0; t < T + 2; ++t) {
-        const int g = it * T + t, b = g & 1;
-        if (t >= 2) {
-          if (!(ok = wait_warp(&bar.p_full[b], ((g - 2) >> 1) & 1, bar.abort))) break;
+    // the whole warp runs this (see mma_ts_lead)
+    const uint32_t lead = elect_one();
+    with_channels(DP / 16, [&](auto ch) {
+      constexpr int kCh = decltype(ch)::value;
+      if constexpr (kSS == (kCh * 16 > kMaxTs)) {
+        const uint32_t kept = smem_u32(smem + mp.kept);
+        Ring ring(mp.stages, 0), last(mp.stages, 0);  // the scores' stage, the gradient products'
+        for (int it = 0; it < n_items; ++it) {
+          if (!wait_warp(bar.a_ready, it & 1, bar.abort)) return false;
           tc_fence_after();
-          const int s = (g - 2) % kS;
-          const uint32_t st = smem_u32(smem + s * mp.stage);
-          issue_grad(tmem + dv_col, tmem + b * kBuf, st + mp.tile, id, t > 2);
-          issue_grad(tmem + dk_col, tmem + b * kBuf + 64, st, id, t > 2);
-          mma_commit_warp(&bar.empty[s]);
-        }
-        if (t < T) {
-          const int s = g % kS;
-          if (!(ok = wait_warp(&bar.full[s], (g / kS) & 1, bar.abort))) break;
-          const uint32_t st = smem_u32(smem + s * mp.stage);
-          const uint32_t kept = smem_u32(smem + mp.kept);
-          issue_scores<kSS>(tmem + b * kBuf, kSS ? kept : tmem + k_col, st, DP / 16);
-          issue_scores<kSS>(tmem + b * kBuf + 64, kSS ? kept + 2 * mp.tile : tmem + v_col, st + mp.tile, DP / 16);
-          mma_commit_warp(&bar.s_full[b]);
+          for (int t = 0; t < T + 2; ++t) {
+            const int g = it * T + t, b = g & 1;
+            // stage full, and P and dL of the tile before last written
+            uint64_t* const full = &bar.full[ring.s];
+            uint64_t* const prev = &bar.p_full[(g - 2) & 7];
+            const uint32_t ph = ring.ph, pp = ((g - 2) >> 3) & 1;
+            if (t < 2       ? t < T && !wait_warp(full, ph, bar.abort)
+                : t < T     ? !wait_warp(full, ph, prev, pp, bar.abort)
+                            : !wait_warp(prev, pp, bar.abort))
+              return false;
+            tc_fence_after();
+            if (t >= 2) {
+              const uint32_t st = smem_u32(smem + last.s * mp.stage);
+              issue_grad<kCh>(tmem + dv_col, tmem + b * kBuf, 32, st + mp.tile, t > 2, lead);
+              issue_grad<kCh>(tmem + dk_col, tmem + b * kBuf + 64, 32, st, t > 2, lead);
+              mma_commit_lead(&bar.empty[last.s], lead);
+              last.step(1);
+            }
+            if (t < T) {
+              const uint32_t st = smem_u32(smem + ring.s * mp.stage);
+              issue_scores<kSS, kCh>(tmem + b * kBuf, kSS ? kept : tmem + k_col, st, lead);
+              issue_scores<kSS, kCh>(tmem + b * kBuf + 64, kSS ? kept + 2 * mp.tile : tmem + v_col, st + mp.tile, lead);
+              mma_commit_lead(&bar.s_full[b], lead);
+              ring.step(1);
+            }
+          }
+          mma_commit_lead(bar.o_done, lead);
         }
       }
-      if (ok) mma_commit_warp(bar.o_done);
-    }
+      return true;
+    });
     drain_mma(bar);
-  } else {
-    const int wg = warp >> 2, buf_wg = wg >> 1, hh = wg & 1;
+  } else if (warp < kComputeWarps) {
+    const int wg = warp >> 2;  // also this warpgroup's buffer
     const int r = ((warp & 3) << 5) | lane;
     const uint32_t lb = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_col = lb + buf_wg * kBuf + 32 * hh, dp_col = s_col + 64;
+    const uint32_t s_col = lb + wg * kBuf, dp_col = s_col + 64;
     // this thread's key in the bias boxes: byte offset of (query row 0, key r),
     // before the row's swizzle of its 16-byte units
-    const int bkey = (r >> 6) * kPanel + (r & 7) * 2, bunit = (r & 63) >> 3;
+    const int bkey = (r >> 6) * kBiasPanel + (r & 7) * 2, bunit = (r & 63) >> 3;
     bool ok = true;
-    auto wait_all = [&](uint64_t* b, uint32_t parity) { return wait_warp(b, parity, bar.abort); };
+    Ring ring(mp.stages, wg);  // this buffer's tiles are every second one
     for (int it = 0; it < n_items; ++it) {
       int bh, h, j0;
       item(it, bh, h, j0);
       const int key = j0 + r;
       const bool valid = key < N;
       const size_t tok = static_cast<size_t>(bh) * N + (valid ? key : 0);
-      if constexpr (!kSS) {
-        if (ok && wg < 2) stage_row((wg ? p.a1 : p.a0) + tok * d, valid, d, DP, lb + (wg ? v_col : k_col));
-        tmem_st_wait();
+      if (ok) {
+        KeptRow kept;
+        load_row(kept, tiled_row(wg ? p.a1 : p.a0, bh, nt, valid ? key : 0, DP), valid, DP);
+        if constexpr (kSS) stage_row_smem(kept, DP, smem + mp.kept + wg * 2 * mp.tile, r);
+        else stage_row(kept, DP, lb + (wg ? v_col : k_col));
       }
+      if constexpr (kSS) fence_proxy_async_smem();
+      else tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar.a_ready);
       const float akj = kBin && valid ? p.ak[static_cast<size_t>(bh) * p.Npad + key] : 0.f;
       const int g0 = it * T;
-      for (int t = (g0 & 1) == buf_wg ? 0 : 1; t < T; t += 2) {  // this buffer's tiles
-        const int g = g0 + t, s = g % kS;
-        ok = ok && wait_all(&bar.s_full[buf_wg], (g >> 1) & 1) && wait_all(&bar.full[s], (g / kS) & 1);
+      for (int t = (g0 & 1) == wg ? 0 : 1; t < T; t += 2, ring.step(2)) {  // this buffer's tiles
+        const int g = g0 + t;
+        ok = ok && wait_warp(&bar.s_full[wg], (g >> 1) & 1, &bar.full[ring.s], ring.ph, bar.abort);
         if (!ok) continue;
         tc_fence_after();
-        const uint8_t* st = smem + s * mp.stage;
-        const float* vec = reinterpret_cast<const float*>(st + mp.vec) + 32 * hh;  // LSE, D at 64, c alpha_q at 128, log2 sum at 192
-        const uint8_t* bt = st + 2 * mp.tile + bkey + 32 * hh * 128;
-        uint32_t xr[32], dp[32];
-        tmem_ld32(s_col, xr);
-        tmem_ld32(dp_col, dp);
-        tmem_ld_wait();
-        uint32_t pp[16], pd[16];
+        const uint8_t* st = smem + ring.s * mp.stage;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 lse = *reinterpret_cast<const float2*>(vec + 2 * e);
-          const float2 D = *reinterpret_cast<const float2*>(vec + 64 + 2 * e);
-          float2 x = reinterpret_cast<float2*>(xr)[e], ci = make_float2(p.cs, p.cs);
-          if constexpr (kBin) {
-            ci = *reinterpret_cast<const float2*>(vec + 128 + 2 * e);
-            x = __fmul2_rn(x, make_float2(akj, akj));
+        for (int hf = 0; hf < 2; ++hf) {
+          // -LSE; -D 64 floats on, c alpha_q 128, -log2 sum 192
+          const float* vec = reinterpret_cast<const float*>(st + mp.vec) + 32 * hf;
+          const uint8_t* bt = st + 2 * mp.tile + bkey + 32 * hf * 128;
+          uint32_t xr[32], dp[32];
+          tmem_ld32(s_col + 32 * hf, xr);
+          tmem_ld32(dp_col + 32 * hf, dp);
+          tmem_ld_wait();
+          uint32_t pp[16], pd[16];
+#pragma unroll
+          for (int e2 = 0; e2 < 8; ++e2) {
+            auto four = [&](int at) { return *reinterpret_cast<const float4*>(vec + at + 4 * e2); };
+            const float4 nlse4 = four(0), nD4 = four(64);
+            float4 ci4 = make_float4(p.cs, p.cs, p.cs, p.cs), nl24 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if constexpr (kBin) ci4 = four(128);
+            if constexpr (kBias) nl24 = four(192);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int e = 2 * e2 + q;
+              auto two = [&](const float4& v) { return q ? make_float2(v.z, v.w) : make_float2(v.x, v.y); };
+              const float2 ci = two(ci4);
+              float2 x = reinterpret_cast<float2*>(xr)[e];
+              if constexpr (kBin) x = __fmul2_rn(x, make_float2(akj, akj));
+              if constexpr (kBias) {
+                auto at = [&](int i) {  // bias of query row i of the half, this thread's key
+                  return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(
+                                             bt + i * 128 + ((bunit ^ (i & 7)) << 4))) << 16);
+                };
+                x = __ffma2_rn(x, ci, make_float2(at(2 * e), at(2 * e + 1)));
+              } else {
+                x = __fmul2_rn(x, ci);
+              }
+              const float2 P = on_fma(e) ? exp2v<kBias, true>(x, two(nlse4), two(nl24))
+                                         : exp2v<kBias>(x, two(nlse4), two(nl24));
+              float2 dl = __fmul2_rn(P, __fadd2_rn(reinterpret_cast<float2*>(dp)[e], two(nD4)));
+              if constexpr (kBin) dl = __fmul2_rn(dl, ci);
+              pp[e] = pack_bf16x2(P.x, P.y);
+              pd[e] = pack_bf16x2(dl.x, dl.y);
+            }
           }
-          if constexpr (kBias) {
-            float2 b;
-            const int e0 = 2 * e, e1 = 2 * e + 1;
-            b.x = __uint_as_float(
-                static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(bt + e0 * 128 + ((bunit ^ (e0 & 7)) << 4))) << 16);
-            b.y = __uint_as_float(
-                static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(bt + e1 * 128 + ((bunit ^ (e1 & 7)) << 4))) << 16);
-            x = __ffma2_rn(x, ci, b);
-          } else {
-            x = __fmul2_rn(x, ci);
-          }
-          float2 nl2 = make_float2(0.f, 0.f);
-          if constexpr (kBias) {
-            nl2 = *reinterpret_cast<const float2*>(vec + 192 + 2 * e);
-            nl2 = make_float2(-nl2.x, -nl2.y);
-          }
-          const float2 P = exp2v<kBias>(x, make_float2(-lse.x, -lse.y), nl2);
-          float2 dl = __fmul2_rn(P, __fadd2_rn(reinterpret_cast<float2*>(dp)[e], make_float2(-D.x, -D.y)));
-          if constexpr (kBin) dl = __fmul2_rn(dl, ci);
-          pp[e] = pack_bf16x2(P.x, P.y);
-          pd[e] = pack_bf16x2(dl.x, dl.y);
+          tmem_st16(s_col + 32 * hf, pp);
+          tmem_st16(dp_col + 32 * hf, pd);
         }
-        tmem_st16(s_col, pp);
-        tmem_st16(dp_col, pd);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bar.p_full[buf_wg]);
+        mbar_arrive(&bar.p_full[g & 7]);
       }
-      ok = ok && wait_all(bar.o_done, it & 1);
+      ok = ok && wait_warp(bar.o_done, it & 1, bar.abort);
       tc_fence_after();
-      if (ok && 32 * wg < d) {
-        store_row(lb + dv_col, 1.f, p.g0 + tok * d, valid, 32 * wg, d);
-        store_row(lb + dk_col, p.out, p.g1 + tok * d, valid, 32 * wg, d);
+      for (int c0 = 32 * wg; ok && c0 < d; c0 += 64) {
+        store_row(lb + dv_col, 1.f, p.g0 + tok * d, valid, c0, d);
+        store_row(lb + dk_col, p.out, p.g1 + tok * d, valid, c0, d);
       }
     }
   }
@@ -700,14 +851,12 @@ inline int dbias_batch(int d) {
 // (dbias_sum_kernel joins them).
 template <bool kBin, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
-dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-             const __grid_constant__ CUtensorMap tm_bias) {
+dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kS = kRowStages;
-  const Map mp = smem_map(p.d, kBias, kS, false, kDbiasScratch);
+  const Map mp = smem_map(p.d, kBias, false, kDbiasScratch + kDbiasOut);
   Bars bar(smem + mp.bars);
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const int N = p.N, d = p.d, DP = (d + 15) / 16 * 16, np = d > 64 ? 2 : 1;
+  const int N = p.N, d = p.d, DP = (d + 15) / 16 * 16, nt = (N + kCols - 1) / kCols;
   const int nit = (N + kRows - 1) / kRows;
   const int npairs = ((N + kCols - 1) / kCols + 1) / 2;  // a last odd tile is paired with one beyond N
   const int G = static_cast<int>(gridDim.x);
@@ -740,73 +889,91 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k, const __g
     if (lane == 0) {
       bool ok = true;
       int g = 0;
+      Ring at_ring(mp.stages, 0);
       for (int it = 0; ok && it < n_items; ++it) {
         const Item x = item(it);
         for (int ch = x.ch0; ok && ch < x.ch1; ++ch) {
           const int nb = batch(ch);
           for (int pr = x.pr0; ok && pr < x.pr1; ++pr) {
-            for (int u = 0; u < 2 * nb; ++u, ++g) {
-              const int s = g % kS, j0 = (2 * pr + (u & 1)) * kCols;
+            for (int u = 0; u < 2 * nb; ++u, ++g, at_ring.step(1)) {
+              const int s = at_ring.s, j0 = (2 * pr + (u & 1)) * kCols;
               const int bh = (ch * p.nb + (u >> 1)) * p.H + x.h;
-              if (g >= kS && !(ok = mbar_wait(&bar.empty[s], ((g / kS) - 1) & 1, bar.abort))) break;
+              if (!(ok = mbar_wait(&bar.empty[s], at_ring.ph ^ 1, bar.abort))) break;  // at once in the first round
               const bool with_bias = kBias && u < 2;  // the first entry's tiles bring the bias
-              // a tile wholly beyond N (the last pair's second) has no alpha_k
-              const bool with_ak = kBin && j0 < N;
+              // a tile wholly beyond N (the last pair's second) is not there: the
+              // stage keeps what it held, and what comes of it is not stored
+              const bool in = j0 < N;
               uint8_t* st = smem + s * mp.stage;
-              mbar_arrive_expect_tx(&bar.full[s], 2u * mp.tile + (with_bias ? kBiasBytes : 0) +
-                                                      (with_ak ? kCols * 4 : 0));
-              for (int c = 0; c < np; ++c) {
-                tma_load_3d(st + c * kPanel, &tm_k, 64 * c, j0, bh, &bar.full[s]);
-                tma_load_3d(st + mp.tile + c * kPanel, &tm_v, 64 * c, j0, bh, &bar.full[s]);
+              const uint32_t bytes = (in ? 2u * mp.tile + (kBin ? kCols * 4 : 0) : 0) + (with_bias ? kBiasBytes : 0);
+              if (bytes) mbar_arrive_expect_tx(&bar.full[s], bytes);
+              else mbar_arrive(&bar.full[s]);
+              if (in) {
+                const size_t at = (static_cast<size_t>(bh) * nt + j0 / kCols) * (mp.tile / 2);
+                bulk_load(st, p.b0 + at, mp.tile, &bar.full[s]);
+                bulk_load(st + mp.tile, p.b1 + at, mp.tile, &bar.full[s]);
+                if constexpr (kBin)
+                  bulk_load(st + mp.vec, p.ak + static_cast<size_t>(bh) * p.Npad + j0, kCols * 4, &bar.full[s]);
               }
               if (with_bias) tma_load_3d(st + 2 * mp.tile, &tm_bias, j0, x.i0, x.h, &bar.full[s]);
-              if (with_ak)
-                bulk_load(st + mp.vec, p.ak + static_cast<size_t>(bh) * p.Npad + j0, kCols * 4, &bar.full[s]);
             }
           }
         }
       }
-      settle(bar, g, kS);
+      settle(bar, g, mp.stages);
     }
   } else if (warp == kMmaWarp) {
-    // the whole warp runs this (see mma_ts_warp)
-    bool ok = true;
-    int g0 = 0, staged = 0;
-    for (int it = 0; ok && it < n_items; ++it) {
-      const Item x = item(it);
-      for (int ch = x.ch0; ok && ch < x.ch1; ++ch, ++staged) {
-        const int nb = batch(ch), T = (x.pr1 - x.pr0) * 2 * nb;
-        if (!(ok = wait_warp(bar.a_ready, staged & 1, bar.abort))) break;
-        tc_fence_after();
-        for (int t = 0; t < T + 2; ++t) {
-          const int g = g0 + t, b = g & 1;
-          if (t >= 2) {
-            if (!(ok = wait_warp(&bar.p_full[b], ((g - 2) >> 1) & 1, bar.abort))) break;
+    // the whole warp runs this (see mma_ts_lead)
+    const uint32_t lead = elect_one();
+    with_channels(DP / 16, [&](auto ch16) {
+      constexpr int kCh = decltype(ch16)::value;
+      int g0 = 0, staged = 0;
+      Ring ring(mp.stages, 0), last(mp.stages, 0);
+      for (int it = 0; it < n_items; ++it) {
+        const Item x = item(it);
+        for (int ch = x.ch0; ch < x.ch1; ++ch, ++staged) {
+          const int nb = batch(ch), T = (x.pr1 - x.pr0) * 2 * nb;
+          if (!wait_warp(bar.a_ready, staged & 1, bar.abort)) return false;
+          tc_fence_after();
+          int e = 0;  // batch entry of the chunk
+          for (int t = 0; t < T + 2; ++t) {
+            const int g = g0 + t, b = g & 1;
+            uint64_t* const full = &bar.full[ring.s];
+            uint64_t* const prev = &bar.p_full[(g - 2) & 7];
+            const uint32_t ph = ring.ph, pp = ((g - 2) >> 3) & 1;
+            if (t < 2       ? t < T && !wait_warp(full, ph, bar.abort)
+                : t < T     ? !wait_warp(full, ph, prev, pp, bar.abort)
+                            : !wait_warp(prev, pp, bar.abort))
+              return false;
             tc_fence_after();
-            if (lane == 0) mbar_arrive(&bar.empty[(g - 2) % kS]);  // its MMAs were complete before the threads read them
+            if (t >= 2) {
+              // its MMAs were complete before the threads read them
+              if (lane == 0) mbar_arrive(&bar.empty[last.s]);
+              last.step(1);
+            }
+            if (t < T) {
+              const uint32_t st = smem_u32(smem + ring.s * mp.stage);
+              issue_scores<false, kCh>(tmem + b * kBuf, tmem + kAcc + e * DP, st, lead);
+              issue_scores<false, kCh>(tmem + b * kBuf + 64, tmem + kAcc + e * DP + DP / 2, st + mp.tile, lead);
+              mma_commit_lead(&bar.s_full[b], lead);
+              ring.step(1);
+              if (b == 1) e = e + 1 == nb ? 0 : e + 1;
+            }
           }
-          if (t < T) {
-            const int s = g % kS, e = (t >> 1) % nb;
-            if (!(ok = wait_warp(&bar.full[s], (g / kS) & 1, bar.abort))) break;
-            const uint32_t st = smem_u32(smem + s * mp.stage);
-            issue_scores<false>(tmem + b * kBuf, tmem + kAcc + e * DP, st, DP / 16);
-            issue_scores<false>(tmem + b * kBuf + 64, tmem + kAcc + e * DP + DP / 2, st + mp.tile, DP / 16);
-            mma_commit_warp(&bar.s_full[b]);
-          }
+          g0 += T;
         }
-        g0 += T;
       }
-    }
+      return true;
+    });
     drain_mma(bar);
-  } else {
-    const int wg = warp >> 2, buf = wg >> 1, hh = wg & 1;
+  } else if (warp < kComputeWarps) {
+    const int wg = warp >> 2;  // also this warpgroup's buffer
     const int r = ((warp & 3) << 5) | lane;
     const uint32_t lb = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_col = lb + buf * kBuf + 32 * hh, dp_col = s_col + 64;
-    float* sc = reinterpret_cast<float*>(smem + mp.scratch);  // [LSE, D, ci, log2 sum][entry of the chunk][128 rows]
+    const uint32_t s_col = lb + wg * kBuf, dp_col = s_col + 64;
+    float* sc = reinterpret_cast<float*>(smem + mp.scratch);  // [-LSE, -D, ci, -log2 sum][entry of the chunk][row]
     bool ok = true;
-    auto wait_all = [&](uint64_t* b, uint32_t parity) { return wait_warp(b, parity, bar.abort); };
-    int g = buf;
+    int g = wg;
+    Ring ring(mp.stages, wg);
     for (int it = 0; it < n_items; ++it) {
       const Item x = item(it);
       const int row = x.i0 + r;
@@ -817,17 +984,19 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k, const __g
         // them), so the kept operands and row vectors may be replaced.
         named_sync(kBar, kCompute);
         if (ok) {
-          for (int u = wg; u < 2 * nb; u += 4) {
-            const size_t tok = (static_cast<size_t>(ch * p.nb + (u >> 1)) * p.H + x.h) * N + (valid ? row : 0);
-            stage_row((u & 1 ? p.a1 : p.a0) + tok * d, valid, d, DP, lb + kAcc + (u >> 1) * DP + (u & 1 ? DP / 2 : 0));
+          for (int u = wg; u < 2 * nb; u += 2) {
+            const int bh = (ch * p.nb + (u >> 1)) * p.H + x.h;
+            KeptRow kept;
+            load_row(kept, tiled_row(u & 1 ? p.a1 : p.a0, bh, nt, valid ? row : 0, DP), valid, DP);
+            stage_row(kept, DP, lb + kAcc + (u >> 1) * DP + (u & 1 ? DP / 2 : 0));
           }
         }
-        if (wg < nb) {
-          const size_t at = (static_cast<size_t>(ch * p.nb + wg) * p.H + x.h) * p.Npad + row;
-          sc[wg * kRows + r] = valid ? p.lse[at] : INFINITY;
-          sc[(4 + wg) * kRows + r] = valid ? p.D[at] : 0.f;
-          sc[(8 + wg) * kRows + r] = !kBin ? p.cs : valid ? p.aq[at] : 0.f;
-          if (kBias) sc[(12 + wg) * kRows + r] = valid ? p.l2[at] : 0.f;
+        for (int u = wg; u < nb; u += 2) {
+          const size_t at = (static_cast<size_t>(ch * p.nb + u) * p.H + x.h) * p.Npad + row;
+          sc[u * kRows + r] = valid ? p.nlse[at] : -INFINITY;
+          sc[(4 + u) * kRows + r] = valid ? p.nD[at] : 0.f;
+          sc[(8 + u) * kRows + r] = !kBin ? p.cs : valid ? p.aq[at] : 0.f;
+          if (kBias) sc[(12 + u) * kRows + r] = valid ? p.nl2[at] : 0.f;
         }
         tmem_st_wait();
         tc_fence_before();
@@ -835,76 +1004,104 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k, const __g
         named_sync(kBar, kCompute);  // the row vectors are in place
         const bool first = ch == x.ch0, last = ch + 1 == x.ch1;
         for (int pr = x.pr0; pr < x.pr1; ++pr) {
-          const int j0 = (2 * pr + buf) * kCols + 32 * hh;  // this thread's first column
-          float2 acc[16];
-          uint32_t bias[16];
+          float2 acc[2][16];
+          uint32_t bias[2][16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[e] = make_float2(0.f, 0.f);
-          for (int b = 0; b < nb; ++b, g += 2) {
-            const int s = g % kS;
-            ok = ok && wait_all(&bar.s_full[buf], (g >> 1) & 1) && wait_all(&bar.full[s], (g / kS) & 1);
+          for (int e = 0; e < 16; ++e) acc[0][e] = acc[1][e] = make_float2(0.f, 0.f);
+          for (int b = 0; b < nb; ++b, g += 2, ring.step(2)) {
+            ok = ok && wait_warp(&bar.s_full[wg], (g >> 1) & 1, &bar.full[ring.s], ring.ph, bar.abort);
             if (!ok) continue;
             tc_fence_after();
-            const uint8_t* st = smem + s * mp.stage;
+            const uint8_t* st = smem + ring.s * mp.stage;
             if (kBias && b == 0) {
-              const uint8_t* br = st + 2 * mp.tile + r * 128;
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const uint4 v = *reinterpret_cast<const uint4*>(br + (((4 * hh + u) ^ (r & 7)) << 4));
-                bias[4 * u] = v.x; bias[4 * u + 1] = v.y; bias[4 * u + 2] = v.z; bias[4 * u + 3] = v.w;
-              }
+              load_bias(st + 2 * mp.tile, r, 0, bias[0]);
+              load_bias(st + 2 * mp.tile, r, 1, bias[1]);
             }
-            const float lse = sc[b * kRows + r], D = sc[(4 + b) * kRows + r], ci = sc[(8 + b) * kRows + r];
-            const float l2 = kBias ? sc[(12 + b) * kRows + r] : 0.f;
-            const float* ak = reinterpret_cast<const float*>(st + mp.vec) + 32 * hh;
+            const float nlse = sc[b * kRows + r], nD = sc[(4 + b) * kRows + r], ci = sc[(8 + b) * kRows + r];
+            const float nl2 = kBias ? sc[(12 + b) * kRows + r] : 0.f;
+            const float* ak = reinterpret_cast<const float*>(st + mp.vec);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < 4; ++q) {  // 16 columns
               uint32_t xr[16], dp[16];
               tmem_ld16(s_col + 16 * q, xr);
               tmem_ld16(dp_col + 16 * q, dp);
               tmem_ld_wait();
-              logits<kBin, kBias, 16>(xr, ak + 16 * q, ci, bias + 8 * q);
+              logits<kBin, kBias, 16>(xr, ak + 16 * q, ci, bias[q >> 1] + 8 * (q & 1));
+              if (q == 3) {  // all of the tile is in registers
+                tc_fence_before();
+                mbar_arrive(&bar.p_full[g & 7]);
+              }
+              float2* to = acc[q >> 1] + 8 * (q & 1);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float2 P =
-                    exp2v<kBias>(reinterpret_cast<float2*>(xr)[e], make_float2(-lse, -lse), make_float2(-l2, -l2));
-                acc[8 * q + e] = __ffma2_rn(P, __fadd2_rn(reinterpret_cast<float2*>(dp)[e], make_float2(-D, -D)),
-                                            acc[8 * q + e]);
+                const float2 xe = reinterpret_cast<float2*>(xr)[e], l0 = make_float2(nlse, nlse), l1 = make_float2(nl2, nl2);
+                const float2 P = on_fma(e) ? exp2v<kBias, true>(xe, l0, l1) : exp2v<kBias>(xe, l0, l1);
+                to[e] = __ffma2_rn(P, __fadd2_rn(reinterpret_cast<float2*>(dp)[e], make_float2(nD, nD)), to[e]);
               }
             }
-            tc_fence_before();
-            mbar_arrive(&bar.p_full[buf]);
           }
-          if (!ok || !valid) continue;
-          const size_t at = (static_cast<size_t>(x.h) * N + row) * N + j0;
-          float* part = p.part ? p.part + static_cast<size_t>(x.split) * p.H * N * N + at : nullptr;
-          const float* a = reinterpret_cast<const float*>(acc);
-          float sum[32];
+          if (!ok) continue;
+          // A warp's 32 rows of 64 bytes go through shared memory (its own 2 KB,
+          // 16-byte units swizzled by the row), so that a store writes whole
+          // 64-byte pieces of a few rows instead of 16 bytes of 32 rows.
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sum[e] = a[e];
-          if (!first) {  // this thread's own sums of the chunks before
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (j0 + e < N) sum[e] += part[e];
-          }
-          if (last && p.nsplit == 1) {
-            uint16_t* dst = p.g0 + at;
-            if (N % 8 == 0) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                if (j0 + e < N)
-                  *reinterpret_cast<uint4*>(dst + e) =
-                      make_uint4(pack_bf16x2(sum[e], sum[e + 1]), pack_bf16x2(sum[e + 2], sum[e + 3]),
-                                 pack_bf16x2(sum[e + 4], sum[e + 5]), pack_bf16x2(sum[e + 6], sum[e + 7]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (j0 + e < N) dst[e] = float_to_bf16_bits(sum[e]);
+          for (int q = 0; q < 2; ++q) {
+            const float* sum = reinterpret_cast<const float*>(acc[q]);
+            const int j0 = (2 * pr + wg) * kCols + 32 * q;  // the half's first column
+            uint8_t* stg = smem + mp.scratch + kDbiasScratch + warp * 2048;
+            auto unit = [&](int row, int u) { return stg + row * 64 + ((u ^ ((row >> 1) & 3)) << 4); };
+            const int r0 = x.i0 + (warp & 3) * 32;
+            const size_t base = (static_cast<size_t>(x.h) * N + r0) * N + j0;  // of the warp's first row
+            if (first && last && p.nsplit == 1) {
+  #pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(unit(lane, k)) =
+                    make_uint4(pack_bf16x2(sum[8 * k], sum[8 * k + 1]), pack_bf16x2(sum[8 * k + 2], sum[8 * k + 3]),
+                               pack_bf16x2(sum[8 * k + 4], sum[8 * k + 5]), pack_bf16x2(sum[8 * k + 6], sum[8 * k + 7]));
+              __syncwarp();
+              if (N % 8 == 0) {
+                const int u = lane & 3;
+  #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int row = 8 * k + (lane >> 2);
+                  if (r0 + row < N && j0 + 8 * u < N)
+                    *reinterpret_cast<uint4*>(p.g0 + base + static_cast<size_t>(row) * N + 8 * u) =
+                        *reinterpret_cast<const uint4*>(unit(row, u));
+                }
+              } else {
+                for (int row = 0; row < 32 && r0 + row < N; ++row)
+                  if (j0 + lane < N)
+                    p.g0[base + static_cast<size_t>(row) * N + lane] =
+                        reinterpret_cast<const uint16_t*>(unit(row, lane >> 3))[lane & 7];
+              }
+              __syncwarp();
+              continue;
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (j0 + e < N) part[e] = sum[e];
+            // fp32 sums over chunks, 16 columns at a time; each element is read,
+            // added to and written by the same thread in every chunk
+            float* part = p.part + static_cast<size_t>(x.split) * p.H * N * N + base;
+            const bool round = last && p.nsplit == 1;
+  #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+  #pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<float4*>(unit(lane, k)) = make_float4(sum[16 * h + 4 * k], sum[16 * h + 4 * k + 1],
+                                                                        sum[16 * h + 4 * k + 2], sum[16 * h + 4 * k + 3]);
+              __syncwarp();
+              const int c0 = 16 * h + (lane & 15);
+  #pragma unroll 4
+              for (int k = 0; k < 16; ++k) {
+                const int row = 2 * k + (lane >> 4);
+                if (r0 + row < N && j0 + c0 < N) {
+                  const size_t at = static_cast<size_t>(row) * N + c0;
+                  float v = reinterpret_cast<const float*>(unit(row, (lane & 15) >> 2))[lane & 3];
+                  if (!first) v += part[at];
+                  if (round) p.g0[base + at] = float_to_bf16_bits(v);
+                  else part[at] = v;
+                }
+              }
+              __syncwarp();
+            }
           }
         }
       }
@@ -924,24 +1121,48 @@ __global__ void __launch_bounds__(256) dbias_sum_kernel(const float* __restrict_
   }
 }
 
-// Binary operands of the tensor cores: the sign words as bf16 +-1 [tokens, d]
-// (d % 8 == 0; one thread per 8 channels), and alpha with rows of N padded to
-// Npad (zeros), times f.
-__global__ void __launch_bounds__(256) expand_signs_kernel(const uint32_t* __restrict__ bits, long long chunks, int d,
-                                                           uint16_t* __restrict__ out) {
-  const int per = d / 8, W = words_for(d);
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < chunks;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    const long long tok = i / per;
-    const int g = static_cast<int>(i - tok * per);
-    const uint32_t byte = bits[tok * W + (g >> 2)] >> (8 * (g & 3));
-    uint32_t w[4];
+// Lays [BH][N][d] tensors out in tiles, [BH][nt][DP / 8 groups][64 rows][8
+// channels] with zeros for rows >= N and channels >= d; blockIdx.y: which of
+// four. A tensor comes as bf16 rows or, sign words, as +-1. Eight rows of four
+// groups per warp, so that both sides move 64 bytes or more at a time.
+struct TileArgs {
+  const uint16_t* rows[4];   // null: bits
+  const uint32_t* bits[4];
+  uint16_t* out[4];
+};
+__global__ void __launch_bounds__(256) tile_kernel(const TileArgs a, int N, int d, int nt, long long units) {
+  const int y = blockIdx.y, groups = (d + 15) / 16 * 2, quads = (groups + 3) / 4;
+  const uint16_t* rows = a.rows[y];
+  const uint32_t* bits = a.bits[y];
+  uint4* out = reinterpret_cast<uint4*>(a.out[y]);
+  const int lane = threadIdx.x & 31, W = words_for(d);
+  // a unit: eight rows of four groups
+  for (long long u = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += gridDim.x * 8ll) {
+    const int gq = static_cast<int>(u % quads);
+    const long long ro = u / quads;  // eight rows
+    const long long tile = ro / (kCols / 8);
+    const int r = static_cast<int>(ro % (kCols / 8)) * 8 + (lane & 7), g = 4 * gq + (lane >> 3);
+    const long long bh = tile / nt;
+    const int n = static_cast<int>(tile % nt) * kCols + r;
+    if (g >= groups) continue;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (n < N && 8 * g < d) {
+      const size_t tok = static_cast<size_t>(bh) * N + n;
+      if (rows) {
+        v = __ldg(reinterpret_cast<const uint4*>(rows + tok * d) + g);
+      } else {
+        const uint32_t byte = __ldg(bits + tok * W + (g >> 2)) >> (8 * (g & 3));
+        uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)  // bf16 1.0 is 0x3F80, -1.0 is 0xBF80
-      w[e] = 0xBF80BF80u ^ (((byte >> (2 * e)) & 1u) << 15) ^ (((byte >> (2 * e + 1)) & 1u) << 31);
-    *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < 4; ++e)  // bf16 1.0 is 0x3F80, -1.0 is 0xBF80
+          w[e] = 0xBF80BF80u ^ (((byte >> (2 * e)) & 1u) << 15) ^ (((byte >> (2 * e + 1)) & 1u) << 31);
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    out[(tile * groups + g) * kCols + r] = v;
   }
 }
+// alpha with rows of N padded to Npad (zeros): alpha_q times c and the units.
 __global__ void __launch_bounds__(256) pad_alpha_kernel(const float* __restrict__ aq, const float* __restrict__ ak,
                                                         long long n, int N, int Npad, float c, float units,
                                                         float* __restrict__ oq, float* __restrict__ ok) {
@@ -956,25 +1177,24 @@ __global__ void __launch_bounds__(256) pad_alpha_kernel(const float* __restrict_
 }
 
 // ------------------------------------------------------------------- host
-// [BH][N][d] bf16 as boxes of 64 channels x 64 rows, or a bias [H][N][N] (rows
-// ld apart) as boxes of 64 keys x box_rows rows; 128-byte swizzle, zeros
-// outside.
-inline bool make_map(CUtensorMap* tm, const uint16_t* base, cuuint64_t inner, cuuint64_t rows, cuuint64_t ld,
-                     cuuint64_t planes, cuuint32_t box_rows, const char* what, std::string* msg) {
+// A bias [H][N][N] (rows ld apart) as boxes of 64 keys x box_rows rows; 128-byte
+// swizzle, zeros outside.
+inline bool make_bias_map(CUtensorMap* tm, const uint16_t* base, cuuint64_t N, cuuint64_t ld, cuuint64_t H,
+                          cuuint32_t box_rows, std::string* msg) {
   tc::EncodeTiledFn enc = tc::encode_fn();
   if (!enc) {
     *msg = "cuTensorMapEncodeTiled entry point unavailable";
     return false;
   }
   const cuuint32_t es[3] = {1, 1, 1};
-  const cuuint64_t dims[3] = {inner, rows, planes};
-  const cuuint64_t strides[2] = {ld * 2, rows * ld * 2};
+  const cuuint64_t dims[3] = {N, N, H};
+  const cuuint64_t strides[2] = {ld * 2, N * ld * 2};
   const cuuint32_t box[3] = {64, box_rows, 1};
   CUresult rc = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (rc != CUDA_SUCCESS) {
-    *msg = std::string("tensor map (") + what + ") rejected: " + std::to_string(rc);
+    *msg = "tensor map (bias) rejected: " + std::to_string(rc);
     return false;
   }
   return true;
@@ -1014,10 +1234,11 @@ inline int npad_for(int N) { return (N + kCols - 1) / kCols * kCols; }
 
 // The workspace of a call, parts rounded up to 256 bytes.
 struct Ws {
-  size_t lse, D, l2, bias, sq, sk, aq, ak, part, total;
+  size_t nlse, nD, nl2, bias, tiled[4], aq, ak, part, total;
 };
 inline Ws workspace(int B, int H, int N, int d, bool bin, bool bias, bool dbias) {
-  const size_t rows = static_cast<size_t>(B) * H * npad_for(N) * 4, x = static_cast<size_t>(B) * H * N * d * 2;
+  const size_t rows = static_cast<size_t>(B) * H * npad_for(N) * 4, 
+               x = static_cast<size_t>(B) * H * npad_for(N) * ((d + 15) / 16 * 16) * 2;
   const DbiasPlan q = dbias_plan(B, H, N, d);
   Ws w;
   size_t at = 0;
@@ -1026,12 +1247,11 @@ inline Ws workspace(int B, int H, int N, int d, bool bin, bool bias, bool dbias)
     at += r256(bytes);
     return here;
   };
-  w.lse = take(rows);
-  w.D = take(rows);
-  w.l2 = take(bias ? rows : 0);
+  w.nlse = take(rows);
+  w.nD = take(rows);
+  w.nl2 = take(bias ? rows : 0);
   w.bias = take(bias && N % 8 ? static_cast<size_t>(H) * N * ((N + 7) / 8 * 8) * 2 : 0);
-  w.sq = take(bin ? x : 0);
-  w.sk = take(bin ? x : 0);
+  for (size_t& t : w.tiled) t = take(x);
   w.aq = take(bin ? rows : 0);
   w.ak = take(bin ? rows : 0);
   w.part = take(dbias && q.nchunks > 1 ? static_cast<size_t>(q.nsplit) * H * N * N * 4 : 0);
@@ -1056,15 +1276,9 @@ inline bool launched(const char* what, std::string* msg) {
   *msg = std::string(what) + " launch: " + cudaGetErrorString(e);
   return false;
 }
-constexpr int kMaxSmem = 227 * 1024;
-
-struct Maps {
-  CUtensorMap q, k, v, dO, bias_rows, bias_cols;
-};
-
 template <bool kBin, bool kBias>
-inline int run(Params p, const Maps& tm, const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* dO,
-               float c, uint16_t* dq, uint16_t* dk, uint16_t* dv, uint16_t* dbias, cudaStream_t st,
+inline int run(Params p, const CUtensorMap& bias_rows, const CUtensorMap& bias_cols, uint16_t* const (&tiled)[4], float c,
+               uint16_t* dq, uint16_t* dk, uint16_t* dv, uint16_t* dbias, cudaStream_t st,
                std::string* msg) {
   const int nsm = sm_count(), nt = (p.N + kRows - 1) / kRows;
   auto grid = [&](int items) { return static_cast<unsigned>(items < nsm ? items : nsm); };
@@ -1073,33 +1287,35 @@ inline int run(Params p, const Maps& tm, const uint16_t* q, const uint16_t* k, c
     static std::atomic<uint64_t> done{0};
     if (!set_smem(rows_kernel<kBin, kBias>, kMaxSmem, done, msg)) return BINATTN_ERR_CUDA;
     Params r = p;
-    r.a0 = q;
-    r.a1 = dO;
+    r.a0 = tiled[0];  // q, k, v, dO
+    r.a1 = tiled[3];
+    r.b0 = tiled[1];
+    r.b1 = tiled[2];
     r.out = c;
     r.g0 = dq;
     r.items = p.B * p.H * nt;
-    rows_kernel<kBin, kBias><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, kRowStages, false, kRowsScratch)),
-                               st>>>(r, tm.k, tm.v, tm.bias_rows);
+    rows_kernel<kBin, kBias><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, false, kRowsScratch)),
+                               st>>>(r, bias_rows);
     if (!launched("rows_kernel", msg)) return BINATTN_ERR_CUDA;
   }
   {
     Params r = p;
-    r.a0 = k;
-    r.a1 = v;
+    r.a0 = tiled[1];
+    r.a1 = tiled[2];
+    r.b0 = tiled[0];
+    r.b1 = tiled[3];
     r.out = kBin ? (kBias ? 1.f : kLn2) : c;  // binary: c alpha_q (and log2 e) are already in dL
     r.g0 = dv;
     r.g1 = dk;
     r.items = p.B * p.H * nt;
-    if (p.d <= 80) {
+    if (p.d <= kMaxTs) {
       static std::atomic<uint64_t> done{0};
       if (!set_smem(cols_kernel<kBin, kBias, false>, kMaxSmem, done, msg)) return BINATTN_ERR_CUDA;
-      cols_kernel<kBin, kBias, false><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, 4, false, 0)), st>>>(
-          r, tm.q, tm.dO, tm.bias_cols, tm.k, tm.v);
+      cols_kernel<kBin, kBias, false><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, false, 0)), st>>>(r, bias_cols);
     } else {
       static std::atomic<uint64_t> done{0};
       if (!set_smem(cols_kernel<kBin, kBias, true>, kMaxSmem, done, msg)) return BINATTN_ERR_CUDA;
-      cols_kernel<kBin, kBias, true><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, 3, true, 0)), st>>>(
-          r, tm.q, tm.dO, tm.bias_cols, tm.k, tm.v);
+      cols_kernel<kBin, kBias, true><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, true, 0)), st>>>(r, bias_cols);
     }
     if (!launched("cols_kernel", msg)) return BINATTN_ERR_CUDA;
   }
@@ -1108,8 +1324,10 @@ inline int run(Params p, const Maps& tm, const uint16_t* q, const uint16_t* k, c
     static std::atomic<uint64_t> done{0};
     if (!set_smem(dbias_kernel<kBin, kBias>, kMaxSmem, done, msg)) return BINATTN_ERR_CUDA;
     Params r = p;
-    r.a0 = q;
-    r.a1 = dO;
+    r.a0 = tiled[0];  // q, k, v, dO
+    r.a1 = tiled[3];
+    r.b0 = tiled[1];
+    r.b1 = tiled[2];
     r.g0 = dbias;
     r.items = plan.items;
     r.nb = plan.nb;
@@ -1117,8 +1335,8 @@ inline int run(Params p, const Maps& tm, const uint16_t* q, const uint16_t* k, c
     r.nsplit = plan.nsplit;
     r.jsplit = plan.jsplit;
     if (plan.nchunks == 1) r.part = nullptr;
-    dbias_kernel<kBin, kBias><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, kRowStages, false, kDbiasScratch)),
-                                st>>>(r, tm.k, tm.v, tm.bias_rows);
+    dbias_kernel<kBin, kBias><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, false, kDbiasScratch + kDbiasOut)),
+                                st>>>(r, bias_rows);
     if (!launched("dbias_kernel", msg)) return BINATTN_ERR_CUDA;
     if (plan.nsplit > 1) {
       const long long n = static_cast<long long>(p.H) * p.N * p.N;
@@ -1138,7 +1356,7 @@ inline int backward(const uint16_t* q, const uint16_t* k, const uint32_t* qb, co
                     cudaStream_t st, std::string* msg) {
   const bool bin = qb != nullptr;
   const Ws w = workspace(B, H, N, d, bin, bias != nullptr, dbias != nullptr);
-  const float units = bias ? 1.f : kLog2e;
+  const float units_of_logits = bias ? 1.f : kLog2e;
   Params p;
   std::memset(&p, 0, sizeof p);
   p.B = B;
@@ -1146,25 +1364,25 @@ inline int backward(const uint16_t* q, const uint16_t* k, const uint32_t* qb, co
   p.N = N;
   p.d = d;
   p.Npad = npad_for(N);
-  p.cs = c * units;
-  p.lse = reinterpret_cast<float*>(ws + w.lse);
-  p.D = reinterpret_cast<float*>(ws + w.D);
-  p.l2 = reinterpret_cast<float*>(ws + w.l2);
+  p.cs = c * units_of_logits;
+  p.nlse = reinterpret_cast<float*>(ws + w.nlse);
+  p.nD = reinterpret_cast<float*>(ws + w.nD);
+  p.nl2 = reinterpret_cast<float*>(ws + w.nl2);
   p.part = reinterpret_cast<float*>(ws + w.part);
+  auto grid = [](long long threads) { return static_cast<unsigned>(std::min<long long>((threads + 255) / 256, 148 * 8)); };
+  const int nt = p.Npad / kCols;
+  uint16_t* tiled[4];
+  for (int i = 0; i < 4; ++i) tiled[i] = reinterpret_cast<uint16_t*>(ws + w.tiled[i]);
+  const long long units = static_cast<long long>(B) * H * nt * (kCols / 8) * (((d + 15) / 16 * 2 + 3) / 4);
+  const TileArgs ta{{q, k, v, dO}, {qb, kb, nullptr, nullptr}, {tiled[0], tiled[1], tiled[2], tiled[3]}};
+  tile_kernel<<<dim3(grid(units * 32), 4), 256, 0, st>>>(ta, N, d, nt, units);
+  if (!launched("tile_kernel", msg)) return BINATTN_ERR_CUDA;
   if (bin) {
-    const long long chunks = static_cast<long long>(B) * H * N * (d / 8);
     const long long n = static_cast<long long>(B) * H * p.Npad;
-    auto grid = [](long long k) { return static_cast<unsigned>(std::min<long long>((k + 255) / 256, 148 * 8)); };
-    uint16_t* sq = reinterpret_cast<uint16_t*>(ws + w.sq);
-    uint16_t* sk = reinterpret_cast<uint16_t*>(ws + w.sk);
     float* aq = reinterpret_cast<float*>(ws + w.aq);
     float* ak = reinterpret_cast<float*>(ws + w.ak);
-    expand_signs_kernel<<<grid(chunks), 256, 0, st>>>(qb, chunks, d, sq);
-    expand_signs_kernel<<<grid(chunks), 256, 0, st>>>(kb, chunks, d, sk);
-    pad_alpha_kernel<<<grid(n), 256, 0, st>>>(alpha_q, alpha_k, n, N, p.Npad, c, units, aq, ak);
-    if (!launched("expand_signs_kernel", msg)) return BINATTN_ERR_CUDA;
-    q = sq;
-    k = sk;
+    pad_alpha_kernel<<<grid(n), 256, 0, st>>>(alpha_q, alpha_k, n, N, p.Npad, c, units_of_logits, aq, ak);
+    if (!launched("pad_alpha_kernel", msg)) return BINATTN_ERR_CUDA;
     p.aq = aq;
     p.ak = ak;
   }
@@ -1176,20 +1394,17 @@ inline int backward(const uint16_t* q, const uint16_t* k, const uint32_t* qb, co
     if (!launched("pad_bias_rows_kernel", msg)) return BINATTN_ERR_CUDA;
     bias = padded;
   }
-  Maps tm;
-  std::memset(&tm, 0, sizeof tm);
-  const cuuint64_t BH = static_cast<cuuint64_t>(B) * H;
-  if (!make_map(&tm.q, q, d, N, d, BH, kCols, "Q", msg) || !make_map(&tm.k, k, d, N, d, BH, kCols, "K", msg) ||
-      !make_map(&tm.v, v, d, N, d, BH, kCols, "V", msg) || !make_map(&tm.dO, dO, d, N, d, BH, kCols, "dO", msg))
-    return BINATTN_ERR_CUDA;
-  if (bias && (!make_map(&tm.bias_rows, bias, N, N, ld, H, kRows, "bias", msg) ||
-               !make_map(&tm.bias_cols, bias, N, N, ld, H, kCols, "bias", msg)))
+  CUtensorMap bias_rows, bias_cols;
+  std::memset(&bias_rows, 0, sizeof bias_rows);
+  std::memset(&bias_cols, 0, sizeof bias_cols);
+  if (bias && (!make_bias_map(&bias_rows, bias, N, ld, H, kRows, msg) ||
+               !make_bias_map(&bias_cols, bias, N, ld, H, kCols, msg)))
     return BINATTN_ERR_CUDA;
   if (bin)
-    return bias ? run<true, true>(p, tm, q, k, v, dO, c, dq, dk, dv, dbias, st, msg)
-                : run<true, false>(p, tm, q, k, v, dO, c, dq, dk, dv, dbias, st, msg);
-  return bias ? run<false, true>(p, tm, q, k, v, dO, c, dq, dk, dv, dbias, st, msg)
-              : run<false, false>(p, tm, q, k, v, dO, c, dq, dk, dv, dbias, st, msg);
+    return bias ? run<true, true>(p, bias_rows, bias_cols, tiled, c, dq, dk, dv, dbias, st, msg)
+                : run<true, false>(p, bias_rows, bias_cols, tiled, c, dq, dk, dv, dbias, st, msg);
+  return bias ? run<false, true>(p, bias_rows, bias_cols, tiled, c, dq, dk, dv, dbias, st, msg)
+              : run<false, false>(p, bias_rows, bias_cols, tiled, c, dq, dk, dv, dbias, st, msg);
 }
 
 }  // namespace bt

@@ -81,7 +81,8 @@ def test_workspace_bytes(size, bin):
     for B, H, N, d in [(1, 1, 1, 8), (2, 16, 4096, 72), (64, 12, 197, 64), (5, 3, 136, 128)]:
         npad = -(-N // 64) * 64
         rows = r(B * H * npad * 4)
-        base = 2 * rows + (2 * r(B * H * N * d * 2) + 2 * rows if bin else 0)
+        # two row vectors, the four operands in tiles, the padded alphas
+        base = 2 * rows + 4 * r(B * H * npad * (-(-d // 16) * 16) * 2) + (2 * rows if bin else 0)
         assert f(B, H, N, d, 0, 0) == base
         pad = r(H * N * (-(-N // 8) * 8) * 2) if N % 8 else 0
         pad += rows  # with a bias the row's sum is kept beside its max
