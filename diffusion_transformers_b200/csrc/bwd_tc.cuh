@@ -61,6 +61,7 @@ constexpr int kCols = 64;                // streamed rows per tile (score MMA N)
 constexpr int kComputeWarps = 8;         // one warpgroup per buffer, one thread per kept row
 constexpr int kMmaWarp = 8, kTmaWarp = 9, kGradWarp = 10;
 constexpr int kThreads = 11 * 32;
+constexpr int kThreadsDbias = 10 * 32;   // one issuing warp: 200 registers a thread instead of 168
 constexpr int kCompute = kComputeWarps * 32;
 constexpr int kGroup = kCols * 16;       // bytes of a tile's 8-channel group
 constexpr int kBiasPanel = 64 * 128;     // bytes of a box of 64 rows x 64 keys of the bias
@@ -269,6 +270,8 @@ struct Map {
 };
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kMaxStages = 8;
+constexpr int kTileBars = 8;             // barriers of tiles in turn; more tiles are never under way than stages
+static_assert(kMaxStages <= kTileBars, "a tile's barrier must be free again before its next tile has a stage");
 constexpr int kBarBytes = 512;
 __host__ __device__ inline Map smem_map(int d, bool bias, bool kept, int scratch) {
   Map m;
@@ -310,8 +313,8 @@ struct Bars {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&p_full[i], kCompute / 2);
     }
+    for (int i = 0; i < kTileBars; ++i) mbar_init(&p_full[i], kCompute / 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&r_full[i], kCompute / 2);
@@ -850,7 +853,7 @@ inline int dbias_batch(int d) {
 // would run, the chunks are also split over CTAs with an array each
 // (dbias_sum_kernel joins them).
 template <bool kBin, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsDbias, 1)
 dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const Map mp = smem_map(p.d, kBias, false, kDbiasScratch + kDbiasOut);
@@ -1335,7 +1338,7 @@ inline int run(Params p, const CUtensorMap& bias_rows, const CUtensorMap& bias_c
     r.nsplit = plan.nsplit;
     r.jsplit = plan.jsplit;
     if (plan.nchunks == 1) r.part = nullptr;
-    dbias_kernel<kBin, kBias><<<grid(r.items), kThreads, bytes(smem_map(p.d, kBias, false, kDbiasScratch + kDbiasOut)),
+    dbias_kernel<kBin, kBias><<<grid(r.items), kThreadsDbias, bytes(smem_map(p.d, kBias, false, kDbiasScratch + kDbiasOut)),
                                 st>>>(r, bias_rows);
     if (!launched("dbias_kernel", msg)) return BINATTN_ERR_CUDA;
     if (plan.nsplit > 1) {
