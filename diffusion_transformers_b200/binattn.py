@@ -8,6 +8,7 @@ ABI cannot see behind its pointers, and runs with that device current.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -413,7 +414,7 @@ def backward_bf16(q_bits: torch.Tensor, k_bits: torch.Tensor, alpha_q: torch.Ten
     dev = _forward_args(q_bits, k_bits, alpha_q, alpha_k, bias, v, None)
     _device(dO, v, workspace)
     need = backward_bf16_workspace_bytes(B, H, N, d, bias is not None, with_dbias)
-    with torch.cuda.device(dev):
+    with _at(dev):
         (dV, ds, dt), dbias, workspace, size = _backward_buffers((B, H, N, d), dev, with_dbias, need, workspace, stream)
         _check(lib().binattn_backward_bf16(_ptr(q_bits), _ptr(k_bits), _ptr(alpha_q), _ptr(alpha_k), _ptr(bias), _ptr(v),
                                            _ptr(dO), float(softmax_scale), B, H, N, d, _ptr(dV), _ptr(ds), _ptr(dt),
@@ -438,7 +439,7 @@ def ref_bf16_backward(q: torch.Tensor, k: torch.Tensor, bias: torch.Tensor | Non
     _expect(bias, "bias", (H, N, N), (torch.bfloat16,))
     dev = _device(q, k, bias, v, dO, workspace)
     need = ref_bf16_backward_workspace_bytes(B, H, N, d, bias is not None, with_dbias)
-    with torch.cuda.device(dev):
+    with _at(dev):
         (dq, dk, dv), dbias, workspace, size = _backward_buffers((B, H, N, d), dev, with_dbias, need, workspace, stream)
         _check(lib().binattn_ref_bf16_backward(_ptr(q), _ptr(k), _ptr(bias), _ptr(v), _ptr(dO), float(softmax_scale), B, H,
                                                N, d, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(workspace), size,
@@ -488,9 +489,16 @@ def _raw(t: torch.Tensor):
 def _on(stream, dev: torch.device):
     """Allocations of a call that runs on `stream` come from that stream's pool,
     so that what the call frees again is not handed to another stream meanwhile."""
-    if stream is not None and stream.device != dev:
+    if stream is None:
+        return contextlib.nullcontext()
+    if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev))
+    return torch.cuda.stream(stream)
+
+
+def _at(dev: torch.device):
+    """`dev` as the current device (at no cost where it is)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _norm_rope_args(q, k, w_q, w_k, cos, sin):
@@ -530,7 +538,7 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor | None, w_k: t
     for name, t in (("q_out", q_out), ("k_out", k_out)):
         _expect(t, name, (B, H, N, d), (q.dtype,))
     dev = _device(q, k, w_q, w_k, cos, sin, q_out, k_out)
-    with torch.cuda.device(dev):
+    with _at(dev):
         with _on(stream, dev):
             q_out, k_out = (torch.empty((B, H, N, d), dtype=q.dtype, device=dev) if t is None else t
                             for t in (q_out, k_out))
@@ -547,7 +555,7 @@ def norm_rope_pack(q: torch.Tensor, k: torch.Tensor, w_q: torch.Tensor | None, w
     alpha_k), the binary forward's inputs. Arguments as norm_rope."""
     (B, H, N, d), dt, strides, cos, sin, rot, per_batch = _norm_rope_args(q, k, w_q, w_k, cos, sin)
     dev = _device(q, k, w_q, w_k, cos, sin)
-    with torch.cuda.device(dev):
+    with _at(dev):
         with _on(stream, dev):
             bits = [torch.empty((B, H, N, _words(d)), dtype=torch.int32, device=dev) for _ in range(2)]
             alpha = [torch.empty((B, H, N), dtype=torch.float32, device=dev) for _ in range(2)]
@@ -578,7 +586,7 @@ def norm_rope_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, d
             _rows(t, name, (B, H, N, d), (q.dtype,))
     dev = _device(q, k, w_q, w_k, cos, sin, dq_out, dk_out, dq, dk, workspace)
     need = 0 if w_q is None and w_k is None else int(lib().binattn_norm_rope_backward_workspace_bytes(B, H, N, d))
-    with torch.cuda.device(dev):
+    with _at(dev):
         with _on(stream, dev):
             dq, dk = (torch.empty((B, H, N, d), dtype=q.dtype, device=dev) if t is None else t for t in (dq, dk))
             dw_q, dw_k = (None if w is None else torch.empty(d, dtype=torch.float32, device=dev) for w in (w_q, w_k))

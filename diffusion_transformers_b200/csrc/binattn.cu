@@ -877,7 +877,7 @@ int binattn_norm_rope_backward(const void* q, const void* k, int dtype, const in
                                        : nr::launch<uint16_t, uint16_t, nr::kOpBwd>(p, inter, vec, st);
   if (int rc = launch_status("norm_rope_backward kernel")) return rc;
   if (p.dwpart) {
-    nr::norm_rope_dw_kernel<<<2, 1024, 0, st>>>(p.dwpart, blocks, d, dw_q, dw_k);
+    nr::norm_rope_dw_kernel<<<dim3(2, (d + 7) / 8), 256, 0, st>>>(p.dwpart, blocks, d, dw_q, dw_k);
     return launch_status("norm_rope_dw_kernel");
   }
   return ok();

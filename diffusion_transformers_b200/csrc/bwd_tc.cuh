@@ -987,11 +987,28 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
         // them), so the kept operands and row vectors may be replaced.
         named_sync(kBar, kCompute);
         if (ok) {
-          for (int u = wg; u < 2 * nb; u += 2) {
-            const int bh = (ch * p.nb + (u >> 1)) * p.H + x.h;
-            KeptRow kept;
-            load_row(kept, tiled_row(u & 1 ? p.a1 : p.a0, bh, nt, valid ? row : 0, DP), valid, DP);
-            stage_row(kept, DP, lb + kAcc + (u >> 1) * DP + (u & 1 ? DP / 2 : 0));
+          // warpgroup 0 the chunk's rows of q, 1 those of dO: half a row of two
+          // entries at a time
+          for (int e = 0; e < nb; e += 2) {
+            for (int g0 = 0; g0 < DP / 8; g0 += 8) {
+              uint4 v[2][8];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint4* src = tiled_row(wg ? p.a1 : p.a0, (ch * p.nb + e + k) * p.H + x.h, nt, row, DP);
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                  v[k][g] = valid && e + k < nb && g0 + g < DP / 8 ? __ldg(src + (g0 + g) * kCols) : make_uint4(0, 0, 0, 0);
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int g = 0; g < 8; g += 2)
+                  if (e + k < nb && g0 + g < DP / 8) {
+                    const uint32_t w[8] = {v[k][g].x,     v[k][g].y,     v[k][g].z,     v[k][g].w,
+                                           v[k][g + 1].x, v[k][g + 1].y, v[k][g + 1].z, v[k][g + 1].w};
+                    tmem_st8(lb + kAcc + (e + k) * DP + (wg ? DP / 2 : 0) + 4 * (g0 + g), w);
+                  }
+            }
           }
         }
         for (int u = wg; u < nb; u += 2) {
@@ -1024,21 +1041,21 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
             const float nl2 = kBias ? sc[(12 + b) * kRows + r] : 0.f;
             const float* ak = reinterpret_cast<const float*>(st + mp.vec);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // 16 columns
-              uint32_t xr[16], dp[16];
-              tmem_ld16(s_col + 16 * q, xr);
-              tmem_ld16(dp_col + 16 * q, dp);
+            for (int q = 0; q < 8; ++q) {  // 8 columns
+              uint32_t xr[8], dp[8];
+              tc2::tmem_ld8(s_col + 8 * q, xr);
+              tc2::tmem_ld8(dp_col + 8 * q, dp);
               tmem_ld_wait();
-              logits<kBin, kBias, 16>(xr, ak + 16 * q, ci, bias[q >> 1] + 8 * (q & 1));
-              if (q == 3) {  // all of the tile is in registers
+              logits<kBin, kBias, 8>(xr, ak + 8 * q, ci, bias[q >> 2] + 4 * (q & 3));
+              if (q == 7) {  // all of the tile is in registers
                 tc_fence_before();
                 mbar_arrive(&bar.p_full[g & 7]);
               }
-              float2* to = acc[q >> 1] + 8 * (q & 1);
+              float2* to = acc[q >> 2] + 4 * (q & 3);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 xe = reinterpret_cast<float2*>(xr)[e], l0 = make_float2(nlse, nlse), l1 = make_float2(nl2, nl2);
-                const float2 P = on_fma(e) ? exp2v<kBias, true>(xe, l0, l1) : exp2v<kBias>(xe, l0, l1);
+              for (int e = 0; e < 4; ++e) {
+                const float2 P =
+                    exp2v<kBias>(reinterpret_cast<float2*>(xr)[e], make_float2(nlse, nlse), make_float2(nl2, nl2));
                 to[e] = __ffma2_rn(P, __fadd2_rn(reinterpret_cast<float2*>(dp)[e], make_float2(nD, nD)), to[e]);
               }
             }
@@ -1213,22 +1230,34 @@ inline int sm_count() {
   return n;
 }
 
-// How dbias is cut up. Chunks of nb batch entries; key splits and then chunk
-// splits until about two items per SM of a 148-SM part run.
+// How dbias is cut up: the batch in chunks of nb entries; then the key splits and
+// chunk splits whose slowest CTA of a 148-SM part has the least to do, counted in
+// tiles: 2 nb per pair of key tiles and chunk, about 4 nb for staging a chunk's
+// operands, 8 for an item. A chunk split costs an fp32 array written and read, so
+// it has to gain a tenth.
 struct DbiasPlan {
   int nb, nchunks, nsplit, jsplit, items;
 };
 inline DbiasPlan dbias_plan(int B, int H, int N, int d) {
-  DbiasPlan q;
-  q.nb = dbias_batch(d);
+  DbiasPlan q{};
+  q.nb = dbias_batch(d) < B ? dbias_batch(d) : B;
   q.nchunks = (B + q.nb - 1) / q.nb;
-  const long long nit = (N + kRows - 1) / kRows;
+  const long long base = static_cast<long long>((N + kRows - 1) / kRows) * H;
   const int npairs = ((N + kCols - 1) / kCols + 1) / 2;
-  const long long base = nit * H;
-  auto up = [](long long a, long long b) { return static_cast<int>((a + b - 1) / b); };
-  q.jsplit = base >= 296 ? 1 : std::min(npairs, up(296, base));
-  q.nsplit = base * q.jsplit >= 296 ? 1 : std::min(q.nchunks, up(296, base * q.jsplit));
-  q.items = static_cast<int>(base * q.jsplit * q.nsplit);
+  auto up = [](long long a, long long b) { return (a + b - 1) / b; };
+  double best = 0;
+  for (int ns = 1; ns <= q.nchunks && ns <= 16; ++ns) {
+    for (int js = 1; js <= npairs && js <= 32; ++js) {
+      const long long item = up(q.nchunks, ns) * q.nb * (2 * up(npairs, js) + 4) + 8;
+      const double cost = static_cast<double>(up(base * ns * js, 148) * item) * (ns > 1 ? 1.1 + 0.01 * ns : 1.0);
+      if (q.items == 0 || cost < best) {
+        best = cost;
+        q.nsplit = ns;
+        q.jsplit = js;
+        q.items = static_cast<int>(base * ns * js);
+      }
+    }
+  }
   return q;
 }
 
@@ -1242,7 +1271,7 @@ struct Ws {
 inline Ws workspace(int B, int H, int N, int d, bool bin, bool bias, bool dbias) {
   const size_t rows = static_cast<size_t>(B) * H * npad_for(N) * 4, 
                x = static_cast<size_t>(B) * H * npad_for(N) * ((d + 15) / 16 * 16) * 2;
-  const DbiasPlan q = dbias_plan(B, H, N, d);
+  const DbiasPlan q = dbias ? dbias_plan(B, H, N, d) : DbiasPlan{};
   Ws w;
   size_t at = 0;
   auto take = [&](size_t bytes) {

@@ -14,15 +14,16 @@
 //   g = dy w,  dx = r (g - r x mean(g r x)).
 // fp32 throughout; each result is rounded once, when it is stored.
 //
-// The pass is bound by memory, so the mapping keeps loads wide and consecutive:
-// d / 8 lanes share a row, each with two quads of 4 channels (8 bytes of bf16,
-// 16 of fp32) chosen so that both members of its four pairs are its own, and
-// 32 / (d / 8) rows share a warp. A lane's channels are the same in every row,
-// so w and the sums of dw stay in registers. One thread per row, as
-// pack_bf16_rows_kernel has it, would cost a strided view 32 cache lines per
-// load. Rows are numbered (batch, token, head) with the head fastest: the rows
-// a block works on share a few tokens' tables. Shapes outside d % 8 == 0,
-// R % 8 == 0 and 4-element alignment take one warp per row and scalar loads.
+// The pass is bound by memory, so the mapping keeps loads wide and the work per
+// row small. A row is d / 8 chunks of 8 channels; a chunk is two quads of 4 (8
+// bytes of bf16, 16 of fp32) chosen so that both members of its four pairs are in
+// it. A lane has kC chunks (the largest of 3, 2, 1 that divides their number), so
+// L = d / 8 / kC lanes share a row and 32 / L rows a warp. A lane's channels are
+// the same in every row, so w and the sums of dw stay in registers. One thread
+// per row, as pack_bf16_rows_kernel has it, would cost a strided view 32 cache
+// lines per load. Rows are numbered (batch, token, head) with the head fastest:
+// the rows a block works on share a few tokens' tables. Shapes outside d % 8 ==
+// 0, R % 8 == 0 and 4-element alignment take one warp per row and scalar loads.
 #pragma once
 #include "common.cuh"
 
@@ -79,15 +80,16 @@ __device__ __forceinline__ void st4(uint16_t* p, float a, float b, float c, floa
   *reinterpret_cast<uint2*>(p) = v;
 }
 
-// Whether p1 - p2 >= 0 for p1 = xa wa c and p2 = xb wb s (the sign of z, since
-// r > 0), exactly. t is their fp32 difference, off by at most 2^-23 (|p1| +
-// |p2|) and 2^-24 |t| from the two or three roundings, so its sign is right
-// beyond 1e-6 (|p1| + |p2|) (and above the range where products underflow);
-// closer to zero the products are taken in 64 bits, in one fixed order, so that
-// equal products cancel to an exact zero.
-__device__ __forceinline__ bool nonneg(float t, float p1, float p2, float xa, float wa, float c, float xb, float wb,
-                                       float s) {
-  if (fabsf(t) > 1e-6f * (fabsf(p1) + fabsf(p2)) && fabsf(t) > 1e-30f) return t > 0.f;
+// The sign of z, since r > 0, is that of p1 - p2 with p1 = xa wa c and p2 = xb wb
+// s. Their fp32 difference t is off by at most 2^-23 (|p1| + |p2|) and 2^-24 |t|
+// from the two or three roundings, so its sign is right beyond 1e-6 (|p1| +
+// |p2|) (and above the range where products underflow); closer to zero the
+// products are taken in 64 bits, in one fixed order, so that equal products
+// cancel to an exact zero, which counts as not negative.
+__device__ __forceinline__ bool clear(float t, float p1, float p2) {
+  return fabsf(t) > fmaf(1e-6f, fabsf(p1) + fabsf(p2), 1e-30f);
+}
+__device__ __forceinline__ bool nonneg64(float xa, float wa, float c, float xb, float wb, float s) {
   const double a = __dmul_rn(__dmul_rn(static_cast<double>(xa), static_cast<double>(wa)), static_cast<double>(c));
   const double b = __dmul_rn(__dmul_rn(static_cast<double>(xb), static_cast<double>(wb)), static_cast<double>(s));
   return __dsub_rn(a, b) >= 0.0;
@@ -113,195 +115,229 @@ __device__ __forceinline__ Row row_of(unsigned long long i, int H, int N, bool s
   return w;
 }
 
-// Sum over the c lanes of this lane's row (pos: its place in the row, base: the
+// Sum over the L lanes of this lane's row (pos: its place in the row, base: the
 // row's first lane), to all of them, in a fixed order.
-__device__ __forceinline__ float row_sum(float v, int c, int pos, int base, bool pow2) {
+__device__ __forceinline__ float row_sum(float v, int L, int pos, int base, bool pow2) {
   if (pow2) {
-    for (int o = 1; o < c; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   }
-  for (int o = 1; o < c; o <<= 1) {
+  for (int o = 1; o < L; o <<= 1) {
     const float u = __shfl_down_sync(0xffffffffu, v, o);
-    if (pos + o < c) v += u;
+    if (pos + o < L) v += u;
   }
   return __shfl_sync(0xffffffffu, v, base);
 }
 
-// T: x's type, G: dz's (backward). kInter: pairs (2p, 2p + 1).
-template <typename T, typename G, int kOp, bool kInter>
+// T: x's type, G: dz's (backward). kInter: pairs (2p, 2p + 1). kC: chunks per lane.
+template <typename T, typename G, int kOp, bool kInter, int kC>
 __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p) {
-  constexpr int kU = 2;  // rows in flight per lane group
   const int t = blockIdx.y;
-  const int d = p.d, H = p.H, N = p.N, half = p.R / 2;
-  const int c = d / 8, rpw = 32 / c;  // lanes per row, rows per warp
+  const int d = p.d, H = p.H, N = p.N, half = p.R / 2, R8 = p.R / 8;
+  const int L = d / 8 / kC, rpw = 32 / L;  // lanes per row, rows per warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = lane / c, pos = lane - grp * c, base = grp * c;
-  const bool pow2 = (c & (c - 1)) == 0;
+  const int grp = lane / L, pos = lane - grp * L, base = grp * L;
+  const bool pow2 = (L & (L - 1)) == 0;
   const bool live = grp < rpw;  // lanes past the last whole row idle
-  const bool turns = pos < p.R / 8;
-  // this lane's two quads: the pairs' first and second members (or, interleaved
-  // or not rotated, eight consecutive channels)
-  const int ca = (kInter || !turns) ? 8 * pos : 4 * pos;
-  const int cb = (kInter || !turns) ? 8 * pos + 4 : half + 4 * pos;
   const T* x = static_cast<const T*>(p.x[t]);
-  // first and second members of the lane's four pairs from its two quads, and back
-  auto split = [&](const float (&qa)[4], const float (&qb)[4], float (&f)[4], float (&s)[4]) {
+  T* out = kOp == kOpPack ? nullptr : static_cast<T*>(p.out[t]);
+  // Chunk k of this lane is chunk j = pos + k L of the row: its two quads are the
+  // first and second members of four pairs, or eight consecutive channels
+  // (interleaved, or not rotated).
+  auto quads = [&](int k, int& ca, int& cb) {
+    const int j = pos + k * L;
+    const bool split = !kInter && j < R8;
+    ca = split ? 4 * j : 8 * j;
+    cb = split ? half + 4 * j : 8 * j + 4;
+  };
+  // first and second members of a chunk's four pairs
+  auto load = [&](const auto* row, int k, float (&f)[4], float (&s)[4]) {
+    int ca, cb;
+    quads(k, ca, cb);
+    float qa[4], qb[4];
+    ld4(row + ca, qa);
+    ld4(row + cb, qb);
     if (kInter) {
       f[0] = qa[0]; s[0] = qa[1]; f[1] = qa[2]; s[1] = qa[3];
       f[2] = qb[0]; s[2] = qb[1]; f[3] = qb[2]; s[3] = qb[3];
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = qa[i], s[i] = qb[i];
+      for (int e = 0; e < 4; ++e) f[e] = qa[e], s[e] = qb[e];
     }
   };
-  float wf[4] = {1.f, 1.f, 1.f, 1.f}, ws[4] = {1.f, 1.f, 1.f, 1.f};
-  if (p.w[t] && live) {
-    float qa[4], qb[4];
-    ld4(p.w[t] + ca, qa);
-    ld4(p.w[t] + cb, qb);
-    split(qa, qb, wf, ws);
+  float wf[kC][4], ws[kC][4], dwf[kC][4], dws[kC][4];
+#pragma unroll
+  for (int k = 0; k < kC; ++k) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) wf[k][e] = ws[k][e] = 1.f, dwf[k][e] = dws[k][e] = 0.f;
+    if (p.w[t] && live) load(p.w[t], k, wf[k], ws[k]);
   }
-  float dwf[4] = {0.f, 0.f, 0.f, 0.f}, dws[4] = {0.f, 0.f, 0.f, 0.f};
 
   const unsigned long long rows = static_cast<unsigned long long>(p.B) * H * N;
-  const bool small = rows <= 0xffffffffull;
   const float inv_d = 1.f / static_cast<float>(d);
-  const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * kWarps * rpw * kU;
-  for (unsigned long long i0 = (static_cast<unsigned long long>(blockIdx.x) * kWarps + warp) * rpw * kU; i0 < rows;
-       i0 += step) {  // the trip count is warp-uniform
-    float xf[kU][4], xs[kU][4], cs[kU][4], sn[kU][4], zf[kU][4], zs[kU][4];
-    Row w[kU];
-    bool in[kU];
+  const unsigned step = gridDim.x * kWarps * rpw;  // rows per round, below 2^32
+  const Row by = row_of(step, H, N, true);         // ... as batch entries, tokens, heads
+  unsigned long long i = (static_cast<unsigned long long>(blockIdx.x) * kWarps + warp) * rpw + grp;
+  Row w = row_of(i, H, N, true);
+  // the trip count is warp-uniform: by the warp's first row
+  for (unsigned long long i0 = i - grp; i0 < rows; i0 += step, i += step) {
+    const bool in = live && i < rows;
+    float xf[kC][4], xs[kC][4], cs[kC][4], sn[kC][4], zf[kC][4], zs[kC][4];
+    const size_t row = (static_cast<size_t>(w.b) * H + w.h) * N + w.n;
+    const T* src = x + w.b * p.xb[t] + w.h * p.xh[t] + w.n * p.xn[t];
+    const size_t tok = (p.per_batch ? static_cast<size_t>(w.b) * N : 0) + w.n;
+    float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const unsigned long long i = i0 + static_cast<unsigned>(u * rpw + grp);
-      in[u] = live && i < rows;
-      w[u] = row_of(in[u] ? i : 0, H, N, small);
+    for (int k = 0; k < kC; ++k) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) xf[u][e] = xs[u][e] = zf[u][e] = zs[u][e] = sn[u][e] = 0.f, cs[u][e] = 1.f;
-      if (in[u]) {
-        float qa[4], qb[4];
-        const T* src = x + w[u].b * p.xb[t] + w[u].h * p.xh[t] + w[u].n * p.xn[t];
-        ld4(src + ca, qa);
-        ld4(src + cb, qb);
-        split(qa, qb, xf[u], xs[u]);
-        if (turns) {
-          const size_t tok = (p.per_batch ? static_cast<size_t>(w[u].b) * N : 0) + w[u].n;
-          ld4(p.cosv + tok * half + 4 * pos, cs[u]);
-          ld4(p.sinv + tok * half + 4 * pos, sn[u]);
+      for (int e = 0; e < 4; ++e) xf[k][e] = xs[k][e] = zf[k][e] = zs[k][e] = sn[k][e] = 0.f, cs[k][e] = 1.f;
+      if (in) {
+        load(src, k, xf[k], xs[k]);
+        if (pos + k * L < R8) {
+          ld4(p.cosv + tok * half + 4 * (pos + k * L), cs[k]);
+          ld4(p.sinv + tok * half + 4 * (pos + k * L), sn[k]);
         }
-        if constexpr (kOp == kOpBwd) {
-          const G* g = static_cast<const G*>(p.dz[t]) + ((static_cast<size_t>(w[u].b) * H + w[u].h) * N + w[u].n) * d;
-          ld4(g + ca, qa);
-          ld4(g + cb, qb);
-          split(qa, qb, zf[u], zs[u]);
-        }
+        if constexpr (kOp == kOpBwd) load(static_cast<const G*>(p.dz[t]) + row * d, k, zf[k], zs[k]);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      float ss = 0.f;
+    for (int k = 0; k < kC; ++k)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ss = fmaf(xf[u][e], xf[u][e], fmaf(xs[u][e], xs[u][e], ss));
-      const float r = rsqrtf(row_sum(ss, c, pos, base, pow2) * inv_d + p.eps);
-      if constexpr (kOp == kOpBwd) {
-        float gf[4], gs[4], dot = 0.f;
+      for (int e = 0; e < 4; ++e) ss = fmaf(xf[k][e], xf[k][e], fmaf(xs[k][e], xs[k][e], ss));
+    const float r = rsqrtf(row_sum(ss, L, pos, base, pow2) * inv_d + p.eps);
+    if constexpr (kOp == kOpBwd) {
+      float dot = 0.f;
+#pragma unroll
+      for (int k = 0; k < kC; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float yf = zf[u][e] * cs[u][e] + zs[u][e] * sn[u][e];
-          const float ys = zs[u][e] * cs[u][e] - zf[u][e] * sn[u][e];
-          const float hf = xf[u][e] * r, hs = xs[u][e] * r;
-          dwf[e] = fmaf(yf, hf, dwf[e]);
-          dws[e] = fmaf(ys, hs, dws[e]);
-          gf[e] = yf * wf[e];
-          gs[e] = ys * ws[e];
-          dot = fmaf(gf[e], hf, fmaf(gs[e], hs, dot));
+          const float yf = zf[k][e] * cs[k][e] + zs[k][e] * sn[k][e];
+          const float ys = zs[k][e] * cs[k][e] - zf[k][e] * sn[k][e];
+          xf[k][e] *= r;
+          xs[k][e] *= r;
+          dwf[k][e] = fmaf(yf, xf[k][e], dwf[k][e]);
+          dws[k][e] = fmaf(ys, xs[k][e], dws[k][e]);
+          zf[k][e] = yf * wf[k][e];
+          zs[k][e] = ys * ws[k][e];
+          dot = fmaf(zf[k][e], xf[k][e], fmaf(zs[k][e], xs[k][e], dot));
         }
-        const float mean = row_sum(dot, c, pos, base, pow2) * inv_d;
+      const float mean = row_sum(dot, L, pos, base, pow2) * inv_d;
+#pragma unroll
+      for (int k = 0; k < kC; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          zf[u][e] = r * (gf[e] - xf[u][e] * r * mean);
-          zs[u][e] = r * (gs[e] - xs[u][e] * r * mean);
+          zf[k][e] = r * (zf[k][e] - xf[k][e] * mean);
+          zs[k][e] = r * (zs[k][e] - xs[k][e] * mean);
         }
-      }
-      if constexpr (kOp == kOpPack) {
-        float sum = 0.f;
-        uint32_t bf = 0, bs = 0;  // sign bits of the four pairs' members
+    }
+    if constexpr (kOp == kOpPack) {
+      float sum = 0.f;
+      uint32_t bits[kC];  // per chunk: the first members' signs, then the second ones'
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        bool sure = true;
+        uint32_t b = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float uf = xf[u][e] * wf[e], us = xs[u][e] * ws[e];
-          const float p1 = uf * cs[u][e], p2 = us * sn[u][e], p3 = us * cs[u][e], p4 = -(uf * sn[u][e]);
-          const float tf = p1 - p2, ts = p3 - p4;
+          const float uf = xf[k][e] * wf[k][e], us = xs[k][e] * ws[k][e];
+          const float p1 = uf * cs[k][e], p2 = us * sn[k][e], p3 = us * cs[k][e], p4 = uf * sn[k][e];
+          const float tf = p1 - p2, ts = p3 + p4;
           sum += fabsf(tf) + fabsf(ts);
-          bf |= (nonneg(tf, p1, p2, xf[u][e], wf[e], cs[u][e], xs[u][e], ws[e], sn[u][e]) ? 1u : 0u) << e;
-          bs |= (nonneg(ts, p3, p4, xs[u][e], ws[e], cs[u][e], xf[u][e], wf[e], -sn[u][e]) ? 1u : 0u) << e;
+          sure = sure && clear(tf, p1, p2) && clear(ts, p3, p4);
+          b |= (tf > 0.f ? 1u : 0u) << e | (ts > 0.f ? 16u : 0u) << e;
         }
-        const float alpha = row_sum(sum, c, pos, base, pow2) * r * inv_d;
-        // byte pos of the row's sign words: channels 8 pos .. 8 pos + 7
+        if (!sure) {  // seldom: some value of the chunk is next to zero
+          b = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            b |= (nonneg64(xf[k][e], wf[k][e], cs[k][e], xs[k][e], ws[k][e], sn[k][e]) ? 1u : 0u) << e;
+            b |= (nonneg64(xs[k][e], ws[k][e], cs[k][e], xf[k][e], wf[k][e], -sn[k][e]) ? 16u : 0u) << e;
+          }
+        }
+        bits[k] = b;
+      }
+      const float alpha = row_sum(sum, L, pos, base, pow2) * r * inv_d;
+      const int wb = 4 * words_for(d);  // bytes per row, the last ones padding
+      uint8_t* dst = reinterpret_cast<uint8_t*>(p.bits[t]) + row * wb;
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        // byte j of the row's sign words: channels 8 j .. 8 j + 7
+        const int j = pos + k * L;
         uint32_t byte;
         if (kInter) {
           byte = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) byte |= ((bf >> e) & 1u) << (2 * e) | ((bs >> e) & 1u) << (2 * e + 1);
+          for (int e = 0; e < 4; ++e) byte |= ((bits[k] >> e) & 1u) << (2 * e) | ((bits[k] >> (4 + e)) & 1u) << (2 * e + 1);
         } else {
-          // quad q of the row is half a byte, held by lane src(q): the lower
-          // half of that lane's pair of nibbles, or the upper
-          const uint32_t mine = bf | bs << 4;
-          const int R8 = p.R / 8;
-          auto src = [&](int q, int& upper) {
+          // quad q of the row is half a byte: the lower half of the chunk that has
+          // it as first members, or the upper half of the one that has it second
+          auto nibble = [&](int q) {
             const bool first = q < R8, second = !first && q < 2 * R8;
-            upper = first ? 0 : second ? 1 : (q & 1);
-            return base + (first ? q : second ? q - R8 : q / 2);
+            const int c = first ? q : second ? q - R8 : q / 2;  // chunk
+            const int ck = c / L;
+            uint32_t v = 0;
+#pragma unroll
+            for (int kk = 0; kk < kC; ++kk) {
+              const uint32_t got = __shfl_sync(0xffffffffu, bits[kk], base + c - ck * L);
+              if (kk == ck) v = got;
+            }
+            return (first ? v : second ? v >> 4 : v >> (4 * (q & 1))) & 0xFu;
           };
-          int u0, u1;
-          const int l0 = src(2 * pos, u0), l1 = src(2 * pos + 1, u1);
-          const uint32_t lo = __shfl_sync(0xffffffffu, mine, l0), hi = __shfl_sync(0xffffffffu, mine, l1);
-          byte = ((lo >> (4 * u0)) & 0xFu) | ((hi >> (4 * u1)) & 0xFu) << 4;
+          byte = nibble(2 * j) | nibble(2 * j + 1) << 4;
         }
-        if (in[u]) {
-          const size_t row = (static_cast<size_t>(w[u].b) * H + w[u].h) * N + w[u].n;
-          const int wb = 4 * words_for(d);  // bytes per row, the last ones padding
-          uint8_t* dst = reinterpret_cast<uint8_t*>(p.bits[t]) + row * wb;
-          dst[pos] = static_cast<uint8_t>(byte);
-          if (pos == 0) {
-            for (int k = c; k < wb; ++k) dst[k] = 0;
-            p.alpha[t][row] = alpha;
-          }
-        }
-      } else {
+        if (in) dst[j] = static_cast<uint8_t>(byte);
+      }
+      if (in && pos == 0) {
+        for (int b = d / 8; b < wb; ++b) dst[b] = 0;
+        p.alpha[t][row] = alpha;
+      }
+    } else if (in) {
+      T* to = out + w.b * p.ob[t] + w.h * p.oh[t] + w.n * p.on[t];
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        float(&f)[4] = zf[k];
+        float(&s)[4] = zs[k];
         if constexpr (kOp == kOpOut) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float yf = xf[u][e] * r * wf[e], ys = xs[u][e] * r * ws[e];
-            zf[u][e] = yf * cs[u][e] - ys * sn[u][e];
-            zs[u][e] = yf * sn[u][e] + ys * cs[u][e];
+            const float yf = xf[k][e] * r * wf[k][e], ys = xs[k][e] * r * ws[k][e];
+            f[e] = yf * cs[k][e] - ys * sn[k][e];
+            s[e] = yf * sn[k][e] + ys * cs[k][e];
           }
         }
-        if (in[u]) {
-          T* dst = static_cast<T*>(p.out[t]) + w[u].b * p.ob[t] + w[u].h * p.oh[t] + w[u].n * p.on[t];
-          const float(&f)[4] = zf[u];
-          const float(&s)[4] = zs[u];
-          if (kInter) {
-            st4(dst + ca, f[0], s[0], f[1], s[1]);
-            st4(dst + cb, f[2], s[2], f[3], s[3]);
-          } else {
-            st4(dst + ca, f[0], f[1], f[2], f[3]);
-            st4(dst + cb, s[0], s[1], s[2], s[3]);
-          }
+        int ca, cb;
+        quads(k, ca, cb);
+        if (kInter) {
+          st4(to + ca, f[0], s[0], f[1], s[1]);
+          st4(to + cb, f[2], s[2], f[3], s[3]);
+        } else {
+          st4(to + ca, f[0], f[1], f[2], f[3]);
+          st4(to + cb, s[0], s[1], s[2], s[3]);
         }
       }
     }
+    // the row `step` further on
+    w.h += by.h;
+    w.n += by.n;
+    w.b += by.b;
+    if (w.h >= H) w.h -= H, ++w.n;
+    if (w.n >= N) w.n -= N, ++w.b;
   }
   if constexpr (kOp == kOpBwd) {
     // the block's sums of dw: every lane group's registers, added in group order
     if (!p.dwpart) return;
-    __shared__ float red[kThreads * 8];  // [group][d]: at most kThreads / c groups of 8 c channels
+    __shared__ float red[kThreads * 8 * kC];  // [group][d]: at most kThreads / L groups of 8 kC L channels
     if (live) {
       float* mine = red + (warp * rpw + grp) * d;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        mine[kInter ? 8 * pos + 2 * e : ca + e] = dwf[e];
-        mine[kInter ? 8 * pos + 2 * e + 1 : cb + e] = dws[e];
+      for (int k = 0; k < kC; ++k) {
+        int ca, cb;
+        quads(k, ca, cb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          mine[kInter ? ca + 2 * e : ca + e] = dwf[k][e];
+          mine[kInter ? ca + 2 * e + 1 : cb + e] = dws[k][e];
+        }
       }
     }
     __syncthreads();
@@ -378,7 +414,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const Params p,
           const float tv = p1 - p2;
           if constexpr (kOp == kOpPack) {
             acc += fabsf(tv);
-            on = nonneg(tv, p1, p2, xv[k], wc, cs, xp, wp, sg);
+            on = clear(tv, p1, p2) ? tv > 0.f : nonneg64(xv[k], wc, cs, xp, wp, sg);
           } else {
             z[k] = tv * r;
           }
@@ -420,29 +456,31 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const Params p,
   }
 }
 
-// dw of q (block 0) and k (block 1) from the blocks' partial sums: 8 slices of
-// the blocks per channel, each added in order, then the slices in order.
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, int blocks, int d,
-                                                            float* dwq, float* dwk) {
-  __shared__ float red[8][128];
-  const int ch = threadIdx.x & 127, slice = threadIdx.x >> 7;
+// dw of q (blockIdx.x 0) and k (1) from the blocks' partial sums, 8 channels per
+// block: 32 slices of the partial sums per channel, each added in order, then the
+// slices in order.
+__global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* __restrict__ part, int blocks, int d,
+                                                           float* dwq, float* dwk) {
+  __shared__ float red[32][8];
+  const int c = threadIdx.x & 7, ch = blockIdx.y * 8 + c, slice = threadIdx.x >> 3;
   const float* src = part + static_cast<size_t>(blockIdx.x) * blocks * d;
   float s = 0.f;
-  if (ch < d)
-    for (int b = slice; b < blocks; b += 8) s += __ldg(src + static_cast<size_t>(b) * d + ch);
-  red[slice][ch] = s;
+  if (ch < d) {
+#pragma unroll 8
+    for (int b = slice; b < blocks; b += 32) s += __ldg(src + static_cast<size_t>(b) * d + ch);
+  }
+  red[slice][c] = s;
   __syncthreads();
   float* out = blockIdx.x ? dwk : dwq;
   if (slice == 0 && ch < d && out) {
-    for (int g = 1; g < 8; ++g) s += red[g][ch];
+    for (int g = 1; g < 32; ++g) s += red[g][c];
     out[ch] = s;
   }
 }
 
-// Blocks per tensor of a launch: each warp's rows at least twice over before a
-// second round of blocks, at most 3 blocks per SM of a 148-SM part and tensor
-// (the kernels stride over the rest; the backward writes one row of partial
-// sums per block).
+// Blocks per tensor of a launch: one round of rows, at most 3 blocks per SM of a
+// 148-SM part and tensor (the kernels stride over the rest; the backward writes
+// one row of partial sums per block).
 constexpr int kMaxBlocks = 148 * 3;
 inline int blocks_for(unsigned long long rows, int rows_per_block) {
   const unsigned long long b = (rows + rows_per_block - 1) / rows_per_block;
@@ -461,15 +499,23 @@ inline bool vec_ok(const Params& p, int es, int gs, bool bwd) {
   return true;
 }
 
+template <typename T, typename G, int kOp, int kC>
+inline int launch_rows(const Params& p, bool inter, cudaStream_t st) {
+  const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.H * p.N;
+  const int blocks = blocks_for(rows, kWarps * (32 / (p.d / 8 / kC)));
+  if (inter) norm_rope_rows_kernel<T, G, kOp, true, kC><<<dim3(blocks, 2), kThreads, 0, st>>>(p);
+  else norm_rope_rows_kernel<T, G, kOp, false, kC><<<dim3(blocks, 2), kThreads, 0, st>>>(p);
+  return blocks;
+}
 template <typename T, typename G, int kOp>
 inline int launch(const Params& p, bool inter, bool vec, cudaStream_t st) {
-  const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.H * p.N;
   if (vec) {
-    const int blocks = blocks_for(rows, kWarps * (32 / (p.d / 8)) * 2);
-    if (inter) norm_rope_rows_kernel<T, G, kOp, true><<<dim3(blocks, 2), kThreads, 0, st>>>(p);
-    else norm_rope_rows_kernel<T, G, kOp, false><<<dim3(blocks, 2), kThreads, 0, st>>>(p);
-    return blocks;
+    const int chunks = p.d / 8;
+    if (chunks % 3 == 0) return launch_rows<T, G, kOp, 3>(p, inter, st);
+    if (chunks % 2 == 0) return launch_rows<T, G, kOp, 2>(p, inter, st);
+    return launch_rows<T, G, kOp, 1>(p, inter, st);
   }
+  const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.H * p.N;
   const int blocks = blocks_for(rows, kWarps);
   norm_rope_any_kernel<T, G, kOp><<<dim3(blocks, 2), kThreads, 0, st>>>(p, inter);
   return blocks;
