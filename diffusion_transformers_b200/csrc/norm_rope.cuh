@@ -19,7 +19,7 @@
 // bytes of bf16, 16 of fp32) chosen so that both members of its four pairs are in
 // it. A lane has kC chunks (the largest of 3, 2, 1 that divides their number), so
 // L = d / 8 / kC lanes share a row and 32 / L rows a warp. A lane's channels are
-// the same in every row, so w and the sums of dw stay in registers. One thread
+// the same in every row, so the sums of dw stay in registers. One thread
 // per row, as pack_bf16_rows_kernel has it, would cost a strided view 32 cache
 // lines per load. Rows are numbered (batch, token, head) with the head fastest:
 // the rows a block works on share a few tokens' tables. Shapes outside d % 8 ==
@@ -58,17 +58,27 @@ __device__ __forceinline__ float ldf(const uint16_t* p) { return bf16_bits_to_fl
 __device__ __forceinline__ void stf(float* p, float v) { *p = v; }
 __device__ __forceinline__ void stf(uint16_t* p, float v) { *p = float_to_bf16_bits(v); }
 
-// Four channels at once.
+// Four channels at once, as they lie in memory and widened.
+template <typename T> struct Quad;
+template <> struct Quad<float> {
+  float4 v;
+  __device__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ void get(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+};
+template <> struct Quad<uint16_t> {
+  uint2 v;
+  __device__ void load(const uint16_t* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ void get(float (&f)[4]) const {
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  }
+};
 __device__ __forceinline__ void ld4(const float* p, float (&f)[4]) {
-  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-}
-__device__ __forceinline__ void ld4(const uint16_t* p, float (&f)[4]) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-  f[0] = __uint_as_float(v.x << 16);
-  f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-  f[2] = __uint_as_float(v.y << 16);
-  f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  Quad<float> q;
+  q.load(p);
+  q.get(f);
 }
 __device__ __forceinline__ void st4(float* p, float a, float b, float c, float d) {
   *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
@@ -131,7 +141,7 @@ __device__ __forceinline__ float row_sum(float v, int L, int pos, int base, bool
 
 // T: x's type, G: dz's (backward). kInter: pairs (2p, 2p + 1). kC: chunks per lane.
 template <typename T, typename G, int kOp, bool kInter, int kC>
-__global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_rows_kernel(const Params p) {
   const int t = blockIdx.y;
   const int d = p.d, H = p.H, N = p.N, half = p.R / 2, R8 = p.R / 8;
   const int L = d / 8 / kC, rpw = 32 / L;  // lanes per row, rows per warp
@@ -151,27 +161,32 @@ __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p
     cb = split ? half + 4 * j : 8 * j + 4;
   };
   // first and second members of a chunk's four pairs
-  auto load = [&](const auto* row, int k, float (&f)[4], float (&s)[4]) {
-    int ca, cb;
-    quads(k, ca, cb);
-    float qa[4], qb[4];
-    ld4(row + ca, qa);
-    ld4(row + cb, qb);
+  auto members = [&](const auto& qa, const auto& qb, float (&f)[4], float (&s)[4]) {
+    float a[4], b[4];
+    qa.get(a);
+    qb.get(b);
     if (kInter) {
-      f[0] = qa[0]; s[0] = qa[1]; f[1] = qa[2]; s[1] = qa[3];
-      f[2] = qb[0]; s[2] = qb[1]; f[3] = qb[2]; s[3] = qb[3];
+      f[0] = a[0]; s[0] = a[1]; f[1] = a[2]; s[1] = a[3];
+      f[2] = b[0]; s[2] = b[1]; f[3] = b[2]; s[3] = b[3];
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = qa[e], s[e] = qb[e];
+      for (int e = 0; e < 4; ++e) f[e] = a[e], s[e] = b[e];
     }
   };
-  float wf[kC][4], ws[kC][4], dwf[kC][4], dws[kC][4];
+  // w in shared memory: it is read once per row, and registers are short
+  __shared__ float4 wsm[32];
+  if (threadIdx.x < d) reinterpret_cast<float*>(wsm)[threadIdx.x] = p.w[t] ? p.w[t][threadIdx.x] : 1.f;
+  __syncthreads();
+  auto weights = [&](int k, float (&f)[4], float (&s)[4]) {
+    int ca, cb;
+    quads(k, ca, cb);
+    members(Quad<float>{wsm[ca / 4]}, Quad<float>{wsm[cb / 4]}, f, s);
+  };
+  float dwf[kC][4], dws[kC][4];
 #pragma unroll
-  for (int k = 0; k < kC; ++k) {
+  for (int k = 0; k < kC; ++k)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) wf[k][e] = ws[k][e] = 1.f, dwf[k][e] = dws[k][e] = 0.f;
-    if (p.w[t] && live) load(p.w[t], k, wf[k], ws[k]);
-  }
+    for (int e = 0; e < 4; ++e) dwf[k][e] = dws[k][e] = 0.f;
 
   const unsigned long long rows = static_cast<unsigned long long>(p.B) * H * N;
   const float inv_d = 1.f / static_cast<float>(d);
@@ -179,12 +194,31 @@ __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p
   const Row by = row_of(step, H, N, true);         // ... as batch entries, tokens, heads
   unsigned long long i = (static_cast<unsigned long long>(blockIdx.x) * kWarps + warp) * rpw + grp;
   Row w = row_of(i, H, N, true);
+  // A row's x (and dz) are loaded, as they lie in memory, while the row before is
+  // worked on: the bytes that are under way bound the pass.
+  Quad<T> xq[2 * kC];
+  Quad<G> zq[kOp == kOpBwd ? 2 * kC : 1];
+  auto fetch = [&](const Row& w) {
+    const T* src = x + w.b * p.xb[t] + w.h * p.xh[t] + w.n * p.xn[t];
+    const G* gz = kOp == kOpBwd ? static_cast<const G*>(p.dz[t]) + ((static_cast<size_t>(w.b) * H + w.h) * N + w.n) * d : nullptr;
+#pragma unroll
+    for (int k = 0; k < kC; ++k) {
+      int ca, cb;
+      quads(k, ca, cb);
+      xq[2 * k].load(src + ca);
+      xq[2 * k + 1].load(src + cb);
+      if constexpr (kOp == kOpBwd) {
+        zq[2 * k].load(gz + ca);
+        zq[2 * k + 1].load(gz + cb);
+      }
+    }
+  };
+  if (live && i < rows) fetch(w);
   // the trip count is warp-uniform: by the warp's first row
   for (unsigned long long i0 = i - grp; i0 < rows; i0 += step, i += step) {
     const bool in = live && i < rows;
     float xf[kC][4], xs[kC][4], cs[kC][4], sn[kC][4], zf[kC][4], zs[kC][4];
     const size_t row = (static_cast<size_t>(w.b) * H + w.h) * N + w.n;
-    const T* src = x + w.b * p.xb[t] + w.h * p.xh[t] + w.n * p.xn[t];
     const size_t tok = (p.per_batch ? static_cast<size_t>(w.b) * N : 0) + w.n;
     float ss = 0.f;
 #pragma unroll
@@ -192,14 +226,29 @@ __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p
 #pragma unroll
       for (int e = 0; e < 4; ++e) xf[k][e] = xs[k][e] = zf[k][e] = zs[k][e] = sn[k][e] = 0.f, cs[k][e] = 1.f;
       if (in) {
-        load(src, k, xf[k], xs[k]);
         if (pos + k * L < R8) {
           ld4(p.cosv + tok * half + 4 * (pos + k * L), cs[k]);
           ld4(p.sinv + tok * half + 4 * (pos + k * L), sn[k]);
         }
-        if constexpr (kOp == kOpBwd) load(static_cast<const G*>(p.dz[t]) + row * d, k, zf[k], zs[k]);
+        members(xq[2 * k], xq[2 * k + 1], xf[k], xs[k]);
+        if constexpr (kOp == kOpBwd) {  // dz turned back
+          members(zq[2 * k], zq[2 * k + 1], zf[k], zs[k]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = zf[k][e] * cs[k][e] + zs[k][e] * sn[k][e];
+            zs[k][e] = zs[k][e] * cs[k][e] - zf[k][e] * sn[k][e];
+            zf[k][e] = y;
+          }
+        }
       }
     }
+    Row next = w;  // the row `step` further on
+    next.h += by.h;
+    next.n += by.n;
+    next.b += by.b;
+    if (next.h >= H) next.h -= H, ++next.n;
+    if (next.n >= N) next.n -= N, ++next.b;
+    if (live && i + step < rows) fetch(next);
 #pragma unroll
     for (int k = 0; k < kC; ++k)
 #pragma unroll
@@ -208,19 +257,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p
     if constexpr (kOp == kOpBwd) {
       float dot = 0.f;
 #pragma unroll
-      for (int k = 0; k < kC; ++k)
+      for (int k = 0; k < kC; ++k) {
+        float wf[4], ws[4];
+        weights(k, wf, ws);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float yf = zf[k][e] * cs[k][e] + zs[k][e] * sn[k][e];
-          const float ys = zs[k][e] * cs[k][e] - zf[k][e] * sn[k][e];
           xf[k][e] *= r;
           xs[k][e] *= r;
-          dwf[k][e] = fmaf(yf, xf[k][e], dwf[k][e]);
-          dws[k][e] = fmaf(ys, xs[k][e], dws[k][e]);
-          zf[k][e] = yf * wf[k][e];
-          zs[k][e] = ys * ws[k][e];
+          dwf[k][e] = fmaf(zf[k][e], xf[k][e], dwf[k][e]);
+          dws[k][e] = fmaf(zs[k][e], xs[k][e], dws[k][e]);
+          zf[k][e] *= wf[e];
+          zs[k][e] *= ws[e];
           dot = fmaf(zf[k][e], xf[k][e], fmaf(zs[k][e], xs[k][e], dot));
         }
+      }
       const float mean = row_sum(dot, L, pos, base, pow2) * inv_d;
 #pragma unroll
       for (int k = 0; k < kC; ++k)
@@ -237,21 +287,23 @@ __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p
       for (int k = 0; k < kC; ++k) {
         bool sure = true;
         uint32_t b = 0;
+        float wf[4], ws[4];
+        weights(k, wf, ws);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float uf = xf[k][e] * wf[k][e], us = xs[k][e] * ws[k][e];
+          const float uf = xf[k][e] * wf[e], us = xs[k][e] * ws[e];
           const float p1 = uf * cs[k][e], p2 = us * sn[k][e], p3 = us * cs[k][e], p4 = uf * sn[k][e];
           const float tf = p1 - p2, ts = p3 + p4;
           sum += fabsf(tf) + fabsf(ts);
           sure = sure && clear(tf, p1, p2) && clear(ts, p3, p4);
           b |= (tf > 0.f ? 1u : 0u) << e | (ts > 0.f ? 16u : 0u) << e;
         }
-        if (!sure) {  // seldom: some value of the chunk is next to zero
+        if (in && !sure) {  // seldom: some value of the chunk is next to zero
           b = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            b |= (nonneg64(xf[k][e], wf[k][e], cs[k][e], xs[k][e], ws[k][e], sn[k][e]) ? 1u : 0u) << e;
-            b |= (nonneg64(xs[k][e], ws[k][e], cs[k][e], xf[k][e], wf[k][e], -sn[k][e]) ? 16u : 0u) << e;
+            b |= (nonneg64(xf[k][e], wf[e], cs[k][e], xs[k][e], ws[e], sn[k][e]) ? 1u : 0u) << e;
+            b |= (nonneg64(xs[k][e], ws[e], cs[k][e], xf[k][e], wf[e], -sn[k][e]) ? 16u : 0u) << e;
           }
         }
         bits[k] = b;
@@ -298,9 +350,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p
         float(&f)[4] = zf[k];
         float(&s)[4] = zs[k];
         if constexpr (kOp == kOpOut) {
+          float wf[4], ws[4];
+          weights(k, wf, ws);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float yf = xf[k][e] * r * wf[k][e], ys = xs[k][e] * r * ws[k][e];
+            const float yf = xf[k][e] * r * wf[e], ys = xs[k][e] * r * ws[e];
             f[e] = yf * cs[k][e] - ys * sn[k][e];
             s[e] = yf * sn[k][e] + ys * cs[k][e];
           }
@@ -316,12 +370,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const Params p
         }
       }
     }
-    // the row `step` further on
-    w.h += by.h;
-    w.n += by.n;
-    w.b += by.b;
-    if (w.h >= H) w.h -= H, ++w.n;
-    if (w.n >= N) w.n -= N, ++w.b;
+    w = next;
   }
   if constexpr (kOp == kOpBwd) {
     // the block's sums of dw: every lane group's registers, added in group order
