@@ -302,7 +302,7 @@ struct Bars {
                          // before the eighth one after it has a stage)
     s_full = b + 24;     // [2] scores and dP of the buffer's tile
     r_full = b + 26;     // [2] its 128 threads hold the tile's scores and dP in registers
-    g_done = b + 28;     // [3] the gradient products from a slot of dL
+    g_done = b + 28;     // [3] the gradient products from a slot of dL (or, over the scores, from a buffer)
     a_ready = b + 31;    // kept operands staged, accumulators read (256 threads)
     o_done = b + 32;     // the item's last MMA
     drain = b + 33;      // [2] an issuing warp's last MMA
@@ -482,13 +482,14 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
           }
         } else {
           for (int t = 0; t < T; ++t, ++g, ring.step(1)) {
-            const int b = g & 1, s = ring.s, slot = kSlots ? g % 3 : b;
+            const int b = g & 1, s = ring.s;
+            const int slot = kSlots ? (it * nkt + t - nkt) % 3 : b;  // slots: by the second pass's tiles
             if (!wait_warp(&bar.p_full[g & 7], (g >> 3) & 1, bar.abort)) return false;
             tc_fence_after();
             if (t >= nkt)
               issue_grad<kCh>(tmem + kAcc, tmem + (kSlots ? p_col + slot * 32 : b * kBuf), kSlots ? 16 : 32,
                               smem_u32(smem + s * mp.stage), t > nkt, lead);
-            mma_commit_lead(&bar.g_done[slot], lead);
+            if (!kSlots || t >= nkt) mma_commit_lead(&bar.g_done[slot], lead);
             mma_commit_lead(&bar.empty[s], lead);
           }
           mma_commit_lead(bar.o_done, lead);
@@ -627,12 +628,15 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
             pk[e] = pack_bf16x2(dl.x, dl.y);
           }
           if (DP <= kMaxTs) {
-            // the slot's last dQ products, three tiles ago, are done with it
-            if (hf == 0 && g >= 3) {
-              if (!(ok = wait_warp(&bar.g_done[g % 3], (g / 3 - 1) & 1, bar.abort))) break;
+            // The slot's last dQ products, those of tile n - 3 of the second
+            // passes, are done with it. (Tile n - 6's are: two tiles ago this
+            // warpgroup waited for tile n - 5's, so the parity tells the two apart.)
+            const int n = it * nkt + t - nkt;
+            if (hf == 0 && n >= 3) {
+              if (!(ok = wait_warp(&bar.g_done[n % 3], (n / 3 - 1) & 1, bar.abort))) break;
               tc_fence_after();
             }
-            tmem_st16(lb + p_col + (g % 3) * 32 + 16 * hf, pk);
+            tmem_st16(lb + p_col + (n % 3) * 32 + 16 * hf, pk);
           } else {
             tmem_st16(s_col + 32 * hf, pk);
           }

@@ -9,7 +9,7 @@ from collections import deque
 
 import pytest
 
-WARPGROUPS = 4
+WARPGROUPS = 2
 
 
 class Barrier:
@@ -56,13 +56,13 @@ class Queue:
             self.q.popleft()()
 
 
-def simulate(kernel, items, nkt, seed, slots=True, stages=4):
+def simulate(kernel, items, nkt, seed, slots=True, stages=4, ring=8):
     rng = random.Random(seed)
     T = 2 * nkt if kernel == "rows" else nkt
     full = [Barrier(1) for _ in range(stages)]
     empty = [Barrier(1) for _ in range(stages)]
-    s_full, r_full = [Barrier(1) for _ in range(2)], [Barrier(2) for _ in range(2)]
-    p_full, g_done = [Barrier(2) for _ in range(4)], [Barrier(1) for _ in range(3)]
+    s_full, r_full = [Barrier(1) for _ in range(2)], [Barrier(1) for _ in range(2)]
+    p_full, g_done = [Barrier(1) for _ in range(ring)], [Barrier(1) for _ in range(3)]
     a_ready, o_done = Barrier(WARPGROUPS), Barrier(1)
     join = {"n": 0, "gen": 0}
     stage = [Cell(f"stage {s}") for s in range(stages)]
@@ -72,6 +72,9 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
     grads_of = (lambda t: t >= nkt) if kernel == "rows" else (lambda t: kernel == "cols")
     done = []
 
+    def where(g):  # the slot of tile g's dL: by second-pass tiles, or its buffer
+        return (g // T * nkt + g % T - nkt) % 3 if slots and kernel == "rows" else g % 2
+
     def tma():
         g = 0
         for _ in range(items):
@@ -79,8 +82,8 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
                 s = g % stages
                 if g >= stages:
                     yield lambda s=s, g=g: empty[s].done(g // stages - 1)
-                # readers: the score products, both warpgroups, and the gradient products
-                n = 3 + bool(grads_of(t))
+                # readers: the score products, the warpgroup, and the gradient products
+                n = 2 + bool(grads_of(t))
 
                 def land(s=s, g=g, n=n):
                     stage[s].write(g, n)
@@ -94,14 +97,14 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
         def run():
             stage[s].read(g)
             # in-place: P / dL over the scores, read by the gradient products too
-            buf[b].write(g, 2)
+            buf[b].write(g, 1)
         q.put(run)
         q.put(s_full[b].arrive)
 
     def issue_grads(q, g, t):
         def run():
             stage[g % stages].read(g)
-            slot[g % 3 if slots and kernel == "rows" else g % 2].read(g)
+            slot[where(g)].read(g)
         if grads_of(t):
             q.put(run)
 
@@ -120,9 +123,10 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
         g = 0
         for _ in range(items):
             for t in range(T):
-                yield lambda g=g: p_full[g % 4].done(g >> 2)
+                yield lambda g=g: p_full[g % ring].done(g // ring)
                 issue_grads(mma2, g, t)
-                mma2.put(g_done[g % 3 if slots else g % 2].arrive)
+                if not slots or grads_of(t):
+                    mma2.put(g_done[where(g)].arrive)
                 mma2.put(empty[g % stages].arrive)
                 g += 1
             mma2.put(o_done.arrive)
@@ -135,7 +139,7 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
                 if t < T:
                     yield lambda g=g: full[g % stages].done(g // stages)
                 if t >= 2:
-                    yield lambda g=g: p_full[(g - 2) % 4].done((g - 2) >> 2)
+                    yield lambda g=g: p_full[(g - 2) % ring].done((g - 2) // ring)
                     issue_grads(mma, g - 2, t - 2)
                     mma.put(empty[(g - 2) % stages].arrive)
                 if t < T:
@@ -149,8 +153,7 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
             join["n"], join["gen"] = 0, gen + 1
         return lambda: join["gen"] > gen
 
-    def group(w):  # one compute warpgroup; tile g belongs to the two of pair g % 2
-        pair, half = w // 2, w % 2
+    def group(w):  # one compute warpgroup: the tiles of its buffer
         for it in range(items):
             if kernel == "dbias":
                 yield meet()
@@ -163,7 +166,7 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
                 if kernel == "rows" and t >= nkt and not joined:
                     joined = True
                     yield meet()
-                if g % 2 != pair:
+                if g % 2 != w:
                     continue
                 yield lambda g=g: s_full[g % 2].done(g >> 1)
                 yield lambda g=g: full[g % stages].done(g // stages)
@@ -173,13 +176,12 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
                     r_full[g % 2].arrive()
                     yield lambda: True
                 if grads_of(t):
-                    which = g % 3 if slots and kernel == "rows" else g % 2
-                    if slots and kernel == "rows" and g >= 3:
-                        yield lambda g=g: g_done[g % 3].done(g // 3 - 1)
-                    if half == 0:
-                        slot[which].write(g, 1)
+                    n = it * nkt + t - nkt
+                    if slots and kernel == "rows" and n >= 3:
+                        yield lambda n=n: g_done[n % 3].done(n // 3 - 1)
+                    slot[where(g)].write(g, 1)
                     yield lambda: True
-                p_full[g % 4].arrive()
+                p_full[g % ring].arrive()
             if kernel == "rows" and not joined:
                 yield meet()
             if kernel != "dbias":
@@ -207,8 +209,8 @@ def simulate(kernel, items, nkt, seed, slots=True, stages=4):
     assert sorted(done) == list(range(WARPGROUPS))
 
 
-@pytest.mark.parametrize("kernel,slots,stages", [("rows", True, 4), ("rows", False, 4), ("cols", False, 4),
-                                                 ("cols", False, 3), ("dbias", False, 4)])
+@pytest.mark.parametrize("kernel,slots,stages", [("rows", True, 8), ("rows", True, 5), ("rows", False, 4), ("cols", False, 8),
+                                                 ("cols", False, 3), ("dbias", False, 5)])
 def test_nothing_waits_for_good_and_nothing_is_overwritten(kernel, slots, stages):
     for seed in range(60):
         for items, nkt in ((1, 1), (3, 1), (2, 2), (3, 3), (2, 5), (1, 9)):
@@ -217,42 +219,13 @@ def test_nothing_waits_for_good_and_nothing_is_overwritten(kernel, slots, stages
             simulate(kernel, items, nkt, seed, slots, stages)
 
 
-def test_the_model_sees_a_parity_overrun(monkeypatch):
-    # p_full by buffer instead of by tile modulo 4: the second issuing warp can
-    # fall two phases behind and waits for good
-    real = Barrier.done
-
-    class Two(list):
-        def __getitem__(self, i):
-            return list.__getitem__(self, i % 2)
-
-    seen = 0
-    for seed in range(200):
+def test_the_model_sees_a_parity_overrun():
+    # the tiles' barriers in a ring of two: the second issuing warp of rows_kernel
+    # can fall two phases behind one of them and then waits for good
+    failed = 0
+    for seed in range(60):
         try:
-            with monkeypatch.context() as m:
-                # a waiter of phase n that looks when n + 1 phases more are complete is late
-                m.setattr(Barrier, "done", lambda self, n: real(self, n) if self.count != 2 else
-                          (self.phase > n and (self.phase - n) % 2 == 1) if seed % 2 else real(self, n))
-                simulate_two(seed)
+            simulate("rows", 2, 9, seed, True, 8, ring=2)
         except AssertionError:
-            seen += 1
-    assert seen
-
-
-def simulate_two(seed):
-    """One producer that may be three tiles ahead of a consumer of two barriers with parities."""
-    rng = random.Random(seed)
-    bars = [Barrier(1), Barrier(1)]
-    produced = consumed = 0
-    idle = 0
-    while consumed < 30:
-        moved = False
-        if produced < 30 and produced - consumed < 4 and rng.random() < 0.7:
-            bars[produced % 2].arrive()
-            produced += 1
-            moved = True
-        if consumed < produced and rng.random() < 0.3 and bars[consumed % 2].done(consumed >> 1):
-            consumed += 1
-            moved = True
-        idle = 0 if moved else idle + 1
-        assert idle < 500
+            failed += 1
+    assert failed
