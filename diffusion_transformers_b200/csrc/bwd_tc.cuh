@@ -259,10 +259,12 @@ __device__ __forceinline__ float2 exp2v(float2 x, float2 minus_top, float2 minus
   if constexpr (kFma) return ex2_fma(y);
   return make_float2(ex2(y.x), ex2(y.y));
 }
-// Every kFmaEvery-th pair of a row's exps runs on the FMA pipe, which the
-// kernels leave half idle, where the special-function unit sets their pace.
-constexpr int kFmaEvery = 4;
-__device__ __forceinline__ constexpr bool on_fma(int pair) { return pair % kFmaEvery == kFmaEvery - 1; }
+// Without a bias every fourth pair of a row's exps runs on the FMA pipe, which has
+// room there beside the special-function unit: 767 against 785 us at 2 x 16 x
+// 4096 x 72 (every second 830, every eighth 773). With a bias the FMA pipe has
+// its share of the logits too, and taking none is best: 1487 against 1510 us.
+template <bool kBias>
+__device__ __forceinline__ constexpr bool on_fma(int pair) { return !kBias && pair % 4 == 3; }
 
 // Shared memory: the stages, then (cols, kSS) the kept operands, then scratch.
 struct Map {
@@ -577,7 +579,7 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 xe = reinterpret_cast<const float2*>(xr)[e];
-            const float2 ex = on_fma(e) ? exp2v<kBias, true>(xe, nm) : exp2v<kBias>(xe, nm);
+            const float2 ex = on_fma<kBias>(e) ? exp2v<kBias, true>(xe, nm) : exp2v<kBias>(xe, nm);
             l2 = __fadd2_rn(l2, ex);
             d2 = __ffma2_rn(ex, reinterpret_cast<const float2*>(dp)[e], d2);
           }
@@ -622,7 +624,7 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 xe = reinterpret_cast<const float2*>(xr)[e];
-            const float2 P = on_fma(e) ? exp2v<kBias, true>(xe, nlse2, nl22) : exp2v<kBias>(xe, nlse2, nl22);
+            const float2 P = on_fma<kBias>(e) ? exp2v<kBias, true>(xe, nlse2, nl22) : exp2v<kBias>(xe, nlse2, nl22);
             float2 dl = __fmul2_rn(P, __fadd2_rn(reinterpret_cast<const float2*>(dp)[e], nD2));
             if constexpr (kBin) dl = __fmul2_rn(dl, *reinterpret_cast<const float2*>(ak + 32 * hf + 2 * e));
             pk[e] = pack_bf16x2(dl.x, dl.y);
@@ -818,7 +820,7 @@ cols_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
               } else {
                 x = __fmul2_rn(x, ci);
               }
-              const float2 P = on_fma(e) ? exp2v<kBias, true>(x, two(nlse4), two(nl24))
+              const float2 P = on_fma<kBias>(e) ? exp2v<kBias, true>(x, two(nlse4), two(nl24))
                                          : exp2v<kBias>(x, two(nlse4), two(nl24));
               float2 dl = __fmul2_rn(P, __fadd2_rn(reinterpret_cast<float2*>(dp)[e], two(nD4)));
               if constexpr (kBin) dl = __fmul2_rn(dl, ci);

@@ -422,14 +422,15 @@ int binattn_backward(const uint32_t *q_bits, const uint32_t *k_bits,
  *   dbias           bf16 [H, N, N], device, written, or NULL.
  *   workspace       device, 16-byte aligned, at least
  *                   binattn_backward_bf16_workspace_bytes(...) bytes: the row
- *                   log-sum-exp and D; the sign words as bf16 +-1 and the
- *                   padded alphas; with N % 8 != 0 a padded copy of the bias;
- *                   and for dbias over more batch entries than one pass sums
- *                   (2 for d > 80, 3 for d > 64, else 4) fp32 sums of
- *                   H * N * N, several times over where H * N is small.
- *                   Overwritten; nothing in it needs to start at zero. Two
- *                   calls that may overlap (other streams, two captured graphs)
- *                   need two workspaces.
+ *                   log-sum-exp and D; copies of the signs (as bf16 +-1), v and
+ *                   dO in the tensor cores' layout and the padded alphas; with a
+ *                   bias and N % 8 != 0 a padded copy of it; and for dbias over
+ *                   more batch entries than one pass sums (2 for d > 80, 3 for
+ *                   d > 64, else 4) fp32 sums of H * N * N, several times over
+ *                   where H * N is small. Overwritten; nothing in it needs to
+ *                   start at zero. Two calls that may overlap (other streams,
+ *                   two captured graphs) need two workspaces.
+ * Outputs must not overlap an input, the workspace or each other.
  * Needs d % 8 == 0 (BINATTN_ERR_UNSUPPORTED otherwise: binattn_backward takes
  * any d). The same call gives the same bits: every sum has one order.
  * Errors as binattn_backward.

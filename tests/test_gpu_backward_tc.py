@@ -246,3 +246,38 @@ def test_long_rows(kind):
     for got, val in ((dq[:, h], scale * dL @ qk[1]), (dk[:, h], scale * dL.transpose(-1, -2) @ qk[0]),
                      (dv[:, h], P.transpose(-1, -2) @ G), (db[h], dL.sum(0))):
         assert (got.to(D) - val).norm() <= 5e-3 * val.norm()
+
+
+def test_many_heads():
+    # the most heads a call takes, each its own item of the kernels
+    B, H, N, d, scale = 4369, 15, 3, 8, 0.3
+    c = make(B, H, N, d, True, seed=13)
+    dq, dk, dv, db = call("ref", c, scale)
+    q, k, v, G = (c[n].double() for n in ("q", "k", "v", "dO"))
+    P = torch.softmax(scale * q @ k.transpose(-1, -2) + c["bias"].double(), -1)
+    dP = G @ v.transpose(-1, -2)
+    dL = P * (dP - (P * dP).sum(-1, keepdim=True))
+    for got, val in ((dq, scale * dL @ k), (dk, scale * dL.transpose(-1, -2) @ q), (dv, P.transpose(-1, -2) @ G),
+                     (db, dL.sum(0))):
+        assert (got.double() - val).norm() <= 5e-3 * val.norm()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_longest_rows(kind):
+    # N = 65535, one head: what holds at any length, and sampled rows in 64 bits
+    N, d, scale = 65535, 64, 0.125
+    c = make(1, 1, N, d, False, seed=14)
+    dq, dk, dv, _ = call(kind, c, scale, with_dbias=False)
+    torch.cuda.synchronize()
+    binattn.device_status()
+    assert ((dv.double().sum(2) - c["dO"].double().sum(2)).abs() <= 2 * 2.0 ** -8 * c["dO"].double().abs().sum(2)).all()
+    qk = [c[n][0, 0].double() for n in "qk"]
+    if kind == "binary":
+        qk = [torch.tensor(ref.signs(b, d)[0, 0], device="cuda") * a[0, 0].double()[:, None]
+              for b, a in (binattn.pack(c[n]) for n in "qk")]
+    rows = torch.tensor([0, 63, 64, 127, 128, 40000, N - 64, N - 1], device="cuda")
+    P = torch.softmax(scale * qk[0][rows] @ qk[1].T, -1)
+    dP = c["dO"][0, 0, rows].double() @ c["v"][0, 0].double().T
+    want_dq = scale * (P * (dP - (P * dP).sum(-1, keepdim=True))) @ qk[1]
+    assert (dq[0, 0, rows].double() - want_dq).norm() <= 5e-3 * want_dq.norm()
+    assert torch.isfinite(dk.float()).all()
