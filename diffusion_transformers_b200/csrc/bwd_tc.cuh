@@ -36,6 +36,16 @@
 // inside a tile. Warps 8 and 10 issue the MMAs, warp 9 the copies. Bounded waits
 // as in fwd_tc2.cuh.
 //
+// Measured on one B200 (GEMM 1614 TFLOP/s, copies 6.5 TB/s). 2 x 16 x 4096 x 72,
+// bf16, without a bias: rows 485 us (five products, 797 TFLOP/s), cols 315 us
+// (four, 982 TFLOP/s). The same binary with a dense bias and dbias: rows 621 us,
+// cols 401 us, dbias 494 us (two products and the bias's read and dbias's write, 2.2
+// TB/s). 64 x 12 x 197 x 64 with a bias: 88, 70 and 147 us. No one unit bounds
+// them: a tile's exps take 512 cycles at 16 per SM and cycle and its products
+// 350 (first pass) to 700 (cols), against 1000 (rows) and 1300 (cols) measured. The
+// rest are the hand-overs of a tile between copies, issuer and compute warps,
+// with two tiles under way per SM.
+//
 // Rounding: P, dL (binary: dL times the alpha of the summed side) and the
 // results to bf16, half a step each; all else fp32.
 #pragma once
@@ -61,7 +71,7 @@ constexpr int kCols = 64;                // streamed rows per tile (score MMA N)
 constexpr int kComputeWarps = 8;         // one warpgroup per buffer, one thread per kept row
 constexpr int kMmaWarp = 8, kTmaWarp = 9, kGradWarp = 10;
 constexpr int kThreads = 11 * 32;
-constexpr int kThreadsDbias = 10 * 32;   // one issuing warp: 200 registers a thread instead of 168
+constexpr int kThreadsDbias = 10 * 32;   // no gradient products, so no warp 10
 constexpr int kCompute = kComputeWarps * 32;
 constexpr int kGroup = kCols * 16;       // bytes of a tile's 8-channel group
 constexpr int kBiasPanel = 64 * 128;     // bytes of a box of 64 rows x 64 keys of the bias
@@ -403,9 +413,12 @@ __device__ __forceinline__ void drain_mma(Bars& b, int which = 0) {
 constexpr int kBuf = 128;         // columns per buffer: scores [0, 64), dP [64, 128)
 constexpr int kAcc = 256;
 constexpr int kMaxTs = 80;        // widest head dim (rounded up to 16) whose operands leave room for slots
-constexpr int kRowsScratch = 3 * 2 * kRows * 4;   // [m, l, sum][warpgroup][row] floats
+constexpr int kRowsScratch = 2 * 3 * 2 * kRows * 4;  // [item's parity][m, l, sum][warpgroup][row] floats
 constexpr int kDbiasScratch = 4 * 4 * kRows * 4;  // [LSE, D, factor, log2 sum][batch entry][row]
-constexpr int kDbiasOut = kComputeWarps * 2048;   // the warps' pieces of the result
+constexpr int kDbiasWarp = 4096;  // a warp's 32 rows of bias; also, at half the size, its piece of the result
+__host__ __device__ constexpr int dbias_scratch(bool bias) {
+  return kDbiasScratch + kComputeWarps * (bias ? kDbiasWarp : kDbiasWarp / 2);
+}
 
 template <bool kBin, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -505,7 +518,6 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
     const int r = ((warp & 3) << 5) | lane;
     const uint32_t lb = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = lb + wg * kBuf, dp_col = s_col + 64;
-    float* sc = reinterpret_cast<float*>(smem + mp.scratch);  // [3][2 warpgroups][128 rows]
     bool ok = true;
     // Half h (32 columns) of the tile at j0: scores as logits (columns >= N as
     // -inf) and dP.
@@ -587,7 +599,10 @@ rows_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
           aD = fmaf(aD, corr, d2.x + d2.y);
         }
       }
-      // ---- the row's two partial results (one per warpgroup) joined
+      // ---- the row's two partial results (one per warpgroup) joined. Items take
+      // turns on two arrays: with one key tile a warpgroup may come to the next
+      // item's join while a thread of the other still reads this one's.
+      float* sc = reinterpret_cast<float*>(smem + mp.scratch) + (it & 1) * 6 * kRows;  // [3][2 warpgroups][128 rows]
       sc[wg * kRows + r] = m;
       sc[(2 + wg) * kRows + r] = l;
       sc[(4 + wg) * kRows + r] = aD;
@@ -862,7 +877,7 @@ template <bool kBin, bool kBias>
 __global__ void __launch_bounds__(kThreadsDbias, 1)
 dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const Map mp = smem_map(p.d, kBias, false, kDbiasScratch + kDbiasOut);
+  const Map mp = smem_map(p.d, kBias, false, dbias_scratch(kBias));
   Bars bar(smem + mp.bars);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int N = p.N, d = p.d, DP = (d + 15) / 16 * 16, nt = (N + kCols - 1) / kCols;
@@ -980,6 +995,8 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
     const uint32_t lb = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = lb + wg * kBuf, dp_col = s_col + 64;
     float* sc = reinterpret_cast<float*>(smem + mp.scratch);  // [-LSE, -D, ci, -log2 sum][entry of the chunk][row]
+    uint8_t* const stg = smem + mp.scratch + kDbiasScratch + warp * (kBias ? kDbiasWarp : kDbiasWarp / 2);
+    uint8_t* const own = stg + lane * 16;  // this thread's bias: 16-byte units 512 apart
     bool ok = true;
     int g = wg;
     Ring ring(mp.stages, wg);
@@ -1031,7 +1048,6 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
         const bool first = ch == x.ch0, last = ch + 1 == x.ch1;
         for (int pr = x.pr0; pr < x.pr1; ++pr) {
           float2 acc[2][16];
-          uint32_t bias[2][16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) acc[0][e] = acc[1][e] = make_float2(0.f, 0.f);
           for (int b = 0; b < nb; ++b, g += 2, ring.step(2)) {
@@ -1040,8 +1056,11 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
             tc_fence_after();
             const uint8_t* st = smem + ring.s * mp.stage;
             if (kBias && b == 0) {
-              load_bias(st + 2 * mp.tile, r, 0, bias[0]);
-              load_bias(st + 2 * mp.tile, r, 1, bias[1]);
+              // kept for the other entries; in registers it would spill
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<uint4*>(own + u * 512) =
+                    *reinterpret_cast<const uint4*>(st + 2 * mp.tile + r * 128 + ((u ^ (r & 7)) << 4));
             }
             const float nlse = sc[b * kRows + r], nD = sc[(4 + b) * kRows + r], ci = sc[(8 + b) * kRows + r];
             const float nl2 = kBias ? sc[(12 + b) * kRows + r] : 0.f;
@@ -1052,7 +1071,10 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
               tc2::tmem_ld8(s_col + 8 * q, xr);
               tc2::tmem_ld8(dp_col + 8 * q, dp);
               tmem_ld_wait();
-              logits<kBin, kBias, 8>(xr, ak + 8 * q, ci, bias[q >> 2] + 4 * (q & 3));
+              uint4 bias = make_uint4(0, 0, 0, 0);
+              if constexpr (kBias) bias = *reinterpret_cast<const uint4*>(own + q * 512);
+              const uint32_t b8[4] = {bias.x, bias.y, bias.z, bias.w};
+              logits<kBin, kBias, 8>(xr, ak + 8 * q, ci, b8);
               if (q == 7) {  // all of the tile is in registers
                 tc_fence_before();
                 mbar_arrive(&bar.p_full[g & 7]);
@@ -1067,14 +1089,14 @@ dbias_kernel(const Params p, const __grid_constant__ CUtensorMap tm_bias) {
             }
           }
           if (!ok) continue;
-          // A warp's 32 rows of 64 bytes go through shared memory (its own 2 KB,
+          __syncwarp();  // the lanes are done with their bias
+          // A warp's 32 rows of 64 bytes go through shared memory (2 KB,
           // 16-byte units swizzled by the row), so that a store writes whole
           // 64-byte pieces of a few rows instead of 16 bytes of 32 rows.
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const float* sum = reinterpret_cast<const float*>(acc[q]);
             const int j0 = (2 * pr + wg) * kCols + 32 * q;  // the half's first column
-            uint8_t* stg = smem + mp.scratch + kDbiasScratch + warp * 2048;
             auto unit = [&](int row, int u) { return stg + row * 64 + ((u ^ ((row >> 1) & 3)) << 4); };
             const int r0 = x.i0 + (warp & 3) * 32;
             const size_t base = (static_cast<size_t>(x.h) * N + r0) * N + j0;  // of the warp's first row
@@ -1373,7 +1395,7 @@ inline int run(Params p, const CUtensorMap& bias_rows, const CUtensorMap& bias_c
     r.nsplit = plan.nsplit;
     r.jsplit = plan.jsplit;
     if (plan.nchunks == 1) r.part = nullptr;
-    dbias_kernel<kBin, kBias><<<grid(r.items), kThreadsDbias, bytes(smem_map(p.d, kBias, false, kDbiasScratch + kDbiasOut)),
+    dbias_kernel<kBin, kBias><<<grid(r.items), kThreadsDbias, bytes(smem_map(p.d, kBias, false, dbias_scratch(kBias))),
                                 st>>>(r, bias_rows);
     if (!launched("dbias_kernel", msg)) return BINATTN_ERR_CUDA;
     if (plan.nsplit > 1) {
