@@ -32,8 +32,9 @@
  *    outputs are untouched. No exception or abort crosses the ABI.
  *    binattn_last_error_message() gives a one-line detail for the calling thread.
  *  - Sizes: B, H, N >= 1; 1 <= d <= 128; B*H <= 65535; N <= 65535.
- *    All pointers must be 16-byte aligned.
- *  - Inputs containing NaN or Inf are outside the contract.
+ *    All pointers must be 16-byte aligned, unless a call says otherwise.
+ *  - Inputs containing NaN or Inf are outside the contract, but for -inf in a
+ *    bias where a call allows it.
  */
 #ifndef BINATTN_H
 #define BINATTN_H
@@ -497,6 +498,7 @@ int binattn_ref_bf16_backward(const uint16_t *q, const uint16_t *k, const uint16
  *   eps        positive.
  *   q_out, k_out  [B, H, N, d] of `dtype`, contiguous, device, written; must
  *              not overlap an input or each other.
+ * The squares are summed in fp32: |x| has to stay below 1e18.
  * Any d in 1..128. d % 8 == 0 and rot % 8 == 0 with addresses and strides of q
  * and k in multiples of 4 elements run at memory speed; other calls take scalar loads.
  * Errors: as binattn_pack; BINATTN_ERR_SHAPE for rot, BINATTN_ERR_ARG for eps
@@ -541,7 +543,7 @@ int binattn_norm_rope_pack(const void *q, const void *k, int dtype, const int64_
  *   dq, dk           [B, H, N, d] of `dtype`, device, aligned to the element,
  *                    written, placed by grad_strides as q and k are by strides
  *                    (so they can be views of the projection's gradient);
- *                    their rows must not overlap each other.
+ *                    no row of them may overlap another one or an input.
  *   dw_q, dw_k       [d] fp32, device, written; NULL skips one. The sums run
  *                    in a fixed order: the same call gives the same bits.
  *   workspace        device, 16-byte aligned, at least
