@@ -39,8 +39,8 @@
 // Measured on one B200 (GEMM 1614 TFLOP/s, copies 6.5 TB/s). 2 x 16 x 4096 x 72,
 // bf16, without a bias: rows 485 us (five products, 797 TFLOP/s), cols 315 us
 // (four, 982 TFLOP/s). The same binary with a dense bias and dbias: rows 621 us,
-// cols 401 us, dbias 494 us (two products and the bias's read and dbias's write, 2.2
-// TB/s). 64 x 12 x 197 x 64 with a bias: 88, 70 and 147 us. No one unit bounds
+// cols 396 us, dbias 433 us (two products and the bias's read and dbias's write, 2.5
+// TB/s). 64 x 12 x 197 x 64 with a bias: 87, 70 and 145 us. No one unit bounds
 // them: a tile's exps take 512 cycles at 16 per SM and cycle and its products
 // 350 (first pass) to 700 (cols), against 1000 (rows) and 1300 (cols) measured. The
 // rest are the hand-overs of a tile between copies, issuer and compute warps,
