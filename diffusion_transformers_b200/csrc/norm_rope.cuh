@@ -101,16 +101,20 @@ __device__ __forceinline__ void st4(uint16_t* p, float a, float b, float c, floa
 // The sign of z, since r > 0, is that of p1 - p2 with p1 = xa wa c and p2 = xb wb
 // s. Their fp32 difference t is off by at most 2^-23 (|p1| + |p2|) and 2^-24 |t|
 // from the two or three roundings, so its sign is right beyond 1e-6 (|p1| +
-// |p2|) (and above the range where products underflow); closer to zero the
-// products are taken in 64 bits, in one fixed order, so that equal products
-// cancel to an exact zero, which counts as not negative.
+// |p2|) (and above the range where products underflow); closer to zero it is
+// decided exactly. A product of three fp32 numbers has up to 72 bits: x w fits
+// in 64-bit arithmetic, times c it is a rounded product and its rounding error,
+// both exact (their lowest bit is no lower than 2^-447). Rounding is monotone, so
+// the rounded products decide unless they are equal, and then the errors do.
+// Equal products give zero, which counts as not negative.
 __device__ __forceinline__ bool clear(float t, float p1, float p2) {
   return fabsf(t) > fmaf(1e-6f, fabsf(p1) + fabsf(p2), 1e-30f);
 }
-__device__ __forceinline__ bool nonneg64(float xa, float wa, float c, float xb, float wb, float s) {
-  const double a = __dmul_rn(__dmul_rn(static_cast<double>(xa), static_cast<double>(wa)), static_cast<double>(c));
-  const double b = __dmul_rn(__dmul_rn(static_cast<double>(xb), static_cast<double>(wb)), static_cast<double>(s));
-  return __dsub_rn(a, b) >= 0.0;
+__device__ __forceinline__ bool nonneg_exact(float xa, float wa, float c, float xb, float wb, float s) {
+  const double u = __dmul_rn(static_cast<double>(xa), static_cast<double>(wa)), cd = static_cast<double>(c);
+  const double v = __dmul_rn(static_cast<double>(xb), static_cast<double>(wb)), sd = static_cast<double>(s);
+  const double a = __dmul_rn(u, cd), b = __dmul_rn(v, sd);
+  return a != b ? a > b : __fma_rn(u, cd, -a) >= __fma_rn(v, sd, -b);
 }
 
 // The token of row i (batch, token, head with the head fastest).
@@ -310,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_rows_kernel(const Param
           b = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            b |= (nonneg64(xf[k][e], wf[e], cs[k][e], xs[k][e], ws[e], sn[k][e]) ? 1u : 0u) << e;
-            b |= (nonneg64(xs[k][e], ws[e], cs[k][e], xf[k][e], wf[e], -sn[k][e]) ? 16u : 0u) << e;
+            b |= (nonneg_exact(xf[k][e], wf[e], cs[k][e], xs[k][e], ws[e], sn[k][e]) ? 1u : 0u) << e;
+            b |= (nonneg_exact(xs[k][e], ws[e], cs[k][e], xf[k][e], wf[e], -sn[k][e]) ? 16u : 0u) << e;
           }
         }
         bits[k] = b;
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const Params p,
           const float tv = p1 - p2;
           if constexpr (kOp == kOpPack) {
             acc += fabsf(tv);
-            on = clear(tv, p1, p2) ? tv > 0.f : nonneg64(xv[k], wc, cs, xp, wp, sg);
+            on = clear(tv, p1, p2) ? tv > 0.f : nonneg_exact(xv[k], wc, cs, xp, wp, sg);
           } else {
             z[k] = tv * r;
           }

@@ -515,7 +515,7 @@ int binattn_norm_rope(const void *q, const void *k, int dtype, const int64_t *st
  * binattn_norm_rope_pack — binattn_norm_rope ended in binattn_pack's output:
  * bits and alpha of the unrounded z of q and of k, in one pass, with no z
  * written. A bit is 1 exactly when x_a w_a cos - x_b w_b sin >= 0 (and
- * likewise for the pair's second member), decided in 64-bit products where 32
+ * likewise for the pair's second member), decided without rounding where 32
  * bits cannot tell; alpha = mean |z|, summed in fp32. (binattn_norm_rope
  * followed by binattn_pack takes alpha from the rounded z.)
  *   q_bits, k_bits    [B, H, N, W] uint32, alpha_q, alpha_k [B, H, N] fp32,
