@@ -8,6 +8,8 @@
 // FlashAttention manner the method's kernel follows (§2 hardware-aware
 // implementation). P stays fp32 here; V is widened from bf16.
 #pragma once
+#include <cfloat>
+
 #include "common.cuh"
 
 namespace binattn {
@@ -41,7 +43,7 @@ fwd_simt_kernel(const uint32_t* __restrict__ qb, const uint32_t* __restrict__ kb
   float o[DMAX];
 #pragma unroll
   for (int c = 0; c < DMAX; ++c) o[c] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  float m = -FLT_MAX, l = 0.f;  // finite: a first key at -inf has no weight
 
   for (int j0 = 0; j0 < N; j0 += kSimtKeys) {
     __syncthreads();
@@ -66,7 +68,7 @@ fwd_simt_kernel(const uint32_t* __restrict__ qb, const uint32_t* __restrict__ kb
       float x = ci * s_ak[jj] * static_cast<float>(s);
       if (kBias) x += bf16_bits_to_float(brow[jj]);
       if (x > m) {
-        const float corr = expf(m - x);  // m = -inf on the first key gives 0
+        const float corr = expf(m - x);  // 0 on the first key (l and o are 0, too)
         l *= corr;
 #pragma unroll
         for (int c = 0; c < DMAX; ++c) o[c] *= corr;
@@ -80,7 +82,7 @@ fwd_simt_kernel(const uint32_t* __restrict__ qb, const uint32_t* __restrict__ kb
     }
   }
   if (active) {
-    const float inv = 1.f / l;
+    const float inv = kBias && l == 0.f ? 0.f : 1.f / l;  // a row of -inf: zero
     uint16_t* orow = out + (tok0 + i) * d;
 #pragma unroll
     for (int c = 0; c < DMAX; ++c)

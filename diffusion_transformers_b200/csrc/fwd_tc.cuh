@@ -76,6 +76,12 @@ constexpr int kExpandThreads = 32;
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 5.545177444479562f;  // 8 * ln 2: rescale O only past 2^8
+// exp(x - m) is one multiply-add whose second product, m log2e, is rounded: a row's
+// weights share a factor of up to 2^64 while |m| is below 2^31 / log2e, which the
+// division by l cancels; beyond it could leave the range. Below this m (masked keys
+// alone so far) m is taken off first. Nor does a max of -inf become an offset: x is
+// -inf then, and every weight 0.
+constexpr float kLowLogit = -1.1e9f;
 
 __host__ __device__ constexpr bool tma_mode_kdim(int kdim) { return kdim <= 80; }
 
@@ -756,9 +762,19 @@ fwd_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_v,
       }
       l *= corr;
       m = m_new;
+      float nm = -m * kLog2e;
+      if constexpr (kBias) {  // see kLowLogit
+        const bool low = m < kLowLogit;
+        if (__any_sync(0xffffffffu, low)) {
+          const float mu = low && m > -INFINITY ? m : 0.f;
+          if (low) nm = 0.f;
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) x[c] -= mu;
+        }
+      }
       // P = exp(logit - m) as bf16 pairs into TMEM over S_t^buf
       const float2 l2e2 = make_float2(kLog2e, kLog2e);
-      const float2 nm2 = make_float2(-m * kLog2e, -m * kLog2e);
+      const float2 nm2 = make_float2(nm, nm);
       float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                       make_float2(0.f, 0.f)};
 #pragma unroll
@@ -783,7 +799,7 @@ fwd_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_v,
     if constexpr (!kDump) {
       if (ok && wait_all(&o_done[t * 2 + ((nkt - 1) & 1)], ((nkt - 1) >> 1) & 1)) {
         tc_fence_after();
-        const float inv = 1.f / l;
+        const float inv = kBias && l == 0.f ? 0.f : 1.f / l;  // a row of -inf: zero
         uint16_t* orow = p.out + (tok0 + row) * d;
 #pragma unroll
         for (int c = 0; c < KDIM; c += 16) {

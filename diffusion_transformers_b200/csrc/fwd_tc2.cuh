@@ -81,6 +81,11 @@ constexpr int kTmemCols = 512;
 constexpr int kQColBin = 224;  // binary Q operand columns (<= 24)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 5.545177444479562f;  // 8 ln 2: rescale only past a 2^8 growth
+// A logit no higher than this is a masked one. (exp(x - m) is one multiply-add whose
+// second product, m log2e, is rounded: the weights of a row share a factor of up to
+// 2^64 at such an m, which the division by l cancels; beyond it could leave the
+// range.)
+constexpr float kNone = -1073741824.f;
 
 // Score sources.
 constexpr int kModeBin = 0;   // binary forward
@@ -224,6 +229,65 @@ __device__ __forceinline__ uint32_t e4m3_bytes(uint32_t word, int j0, int c0, in
   return v;
 }
 
+// The result of a row without any logit above kNone (which is all that the key loop
+// weighs; of other rows it is left alone). Biases that low are 64 or more apart in
+// fp32 and the scores vanish beside them, so the weights are 1 where the row's bias
+// (brow, of the CTA's keys) is largest and 0 elsewhere, and none at -inf: then the
+// result is 0. Written to orow or, for a key half, to part (values 2 kRows apart: the
+// sum, its max, the sum of the weights). It runs behind everything else: inside the
+// key loop or its epilogue the same work cost ordinary rows 1 to 7% (283.8 us at 2 x
+// 16 x 4096 x 72 with this; 290 to 304 in the loop).
+__device__ __forceinline__ void masked_row(const uint16_t* brow, const uint16_t* v, int keys, int d, uint16_t* orow,
+                                        float* part) {
+  // the biases of keys j .. j + 7 (rows are padded to a multiple of 8)
+  auto load = [&](int j, float (&b)[8]) {
+    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(brow + j));
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+      b[e] = j + e < keys ? x : -INFINITY;
+    }
+  };
+  float top = -INFINITY, n = 0.f, b[8];
+  for (int j = 0; j < keys; j += 8) {
+    load(j, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, b[e]);
+    if (top > kNone) return;
+  }
+  for (int c = 0; c < d; c += 8) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    n = 0.f;
+    for (int j = 0; j < keys && top > -INFINITY; j += 8) {
+      load(j, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (b[e] == top) {
+          n += 1.f;
+          const uint4 raw = __ldg(reinterpret_cast<const uint4*>(v + static_cast<size_t>(j + e) * d + c));
+          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] += __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+        }
+      }
+    }
+    if (part) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) part[(c + k) * (2 * kRows)] = o[k];
+    } else {
+      const float inv = n > 0.f ? 1.f / n : 0.f;
+      *reinterpret_cast<uint4*>(orow + c) =
+          make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                     pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+    }
+  }
+  if (part) {
+    part[d * (2 * kRows)] = top;
+    part[(d + 1) * (2 * kRows)] = n;
+  }
+}
+
 template <int DV, int kMode, int kBiasKind>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
@@ -237,6 +301,7 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
   constexpr bool kDump = kMode == kModeDump;
   constexpr bool kMax = kMode == kModeMax;
   constexpr bool kI8 = kMode == kModeI8;
+  constexpr bool kMasks = kBias && (kMode == kModeBin || kRef);  // rows may have nothing but masked logits
   constexpr bool kF16PV = kMode == kModeBin || kRef;  // bf16 P.V from TMA-loaded V
   constexpr bool kNoPV = kDump || kMax;
   constexpr int kKS = L::kKS, kBS = L::kBS;
@@ -257,6 +322,7 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
   uint64_t* q_ready = bars + 46;   // [2 t] softmax t staged the pair's Q_t (128 arrivals) -> issuer t
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  volatile int* masked = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);  // a row came out without weights
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Work items are 256-row pairs, numbered b fastest, then the query tile,
@@ -344,6 +410,7 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
     mbar_init(&q_ready[0], kSoftmaxPerTile);
     mbar_init(&q_ready[1], kSoftmaxPerTile);
     *abort = 0;
+    *masked = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp0) {
@@ -627,7 +694,11 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
     bool row_valid = false;
     size_t tok0 = 0;
     float ci = 0.f;
-    float m = -INFINITY;
+    // A dense bias may leave a row, or its first keys, with nothing but masked
+    // logits: while a row has none above kNone, m stays there (finite, so that no
+    // -inf becomes an offset) and its weights are 0; see masked_row.
+    constexpr float kTop = kMasks ? kNone : -INFINITY;
+    float m = kTop;
     bool ok = true;
     // Waits are made warp-uniform: the tcgen05.ld/st below are warp-collective.
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
@@ -799,7 +870,7 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
       ci = kRef ? p.scale : ((!kDump && row_valid) ? p.scale * aq_row : 0.f);
       fetch_qbits(it + 1, qn, aqn);  // in flight through this pair
     }
-    m = -INFINITY;
+    m = kTop;
     if constexpr (kI8) m = row_valid ? p.mrow[tok0 + row] : 0.f;
     if constexpr (kRel) rel_setup();
     for (int kt = 0; kt < nkt; ++kt) {
@@ -865,7 +936,7 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
           if constexpr (kMax) m = fmaxf(m, tmax);
           if (__any_sync(0xffffffffu, grow)) {
             const float m_new = grow ? tmax : m;
-            const float corr = grow ? ex2((m - m_new) * kLog2e) : 1.f;  // 0 while m is -inf
+            const float corr = grow ? ex2((m - m_new) * kLog2e) : 1.f;  // 0 while nothing was above kNone
             if (kt > 0 && (ok = wait_pv_prev(g, kt, it))) {
 #pragma unroll
               for (int cc = 0; cc < DV; cc += 16) {
@@ -949,6 +1020,7 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
         uint32_t lbits;  // l = O_t column d
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(lbits) : "r"(o_col + d));
         tmem_ld_wait();
+        if (kMasks && lbits == 0u) *masked = 1;  // masked_row writes this row again
         if (p.split) {
           // Partial result of this key half: unnormalised O (d fp32), then m, then l.
           // channel-major: value c of row r256 of (pair slot, half) at
@@ -1012,6 +1084,20 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if constexpr (kMasks) {
+    if (*masked && !*abort && threadIdx.x < 2 * kRows) {  // the threads that wrote the rows
+      for (int it = 0; it < n_items; ++it) {
+        const Item w = item(it);
+        const int row = w.q0 + static_cast<int>(threadIdx.x);
+        if (row >= N) continue;
+        const size_t slice = p.bias_per_sample ? w.bh : w.h;
+        const uint16_t* brow = p.bias + (slice * N + row) * (p.bias_ld > 0 ? p.bias_ld : N) + key0;
+        float* part = p.split ? p.part + static_cast<size_t>((blockIdx.x >> 1) * 2 + half) * (d + 2) * (2 * kRows) + threadIdx.x
+                              : nullptr;
+        masked_row(brow, p.v + (w.tok0 + key0) * d, min(N - key0, nkt * kKeys), d, p.out + (w.tok0 + row) * d, part);
+      }
+    }
+  }
 }
 
 // Bias rows padded to ld elements (ld % 8 == 0, pad 0), so that they are TMA
@@ -1072,8 +1158,10 @@ __global__ void __launch_bounds__(256) combine_halves_kernel(const float* __rest
   const float* p1 = p0 + static_cast<size_t>(d + 2) * kS;
   const float m0 = p0[d * kS], m1 = p1[d * kS];
   const float M = fmaxf(m0, m1);
-  const float w0 = ex2((m0 - M) * kLog2e), w1 = ex2((m1 - M) * kLog2e);
-  const float inv = 1.f / (w0 * p0[(d + 1) * kS] + w1 * p1[(d + 1) * kS]);
+  const float Ms = M == -INFINITY ? 0.f : M;  // a row of -inf: no weights, zero
+  const float w0 = ex2((m0 - Ms) * kLog2e), w1 = ex2((m1 - Ms) * kLog2e);
+  const float l = w0 * p0[(d + 1) * kS] + w1 * p1[(d + 1) * kS];
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* orow = out + ((static_cast<size_t>(b) * H + h) * N + row) * d;
   for (int c = 0; c < d; c += 8) {
     uint32_t w[4];

@@ -123,6 +123,12 @@ int binattn_pack(const void *x, int dtype, int B, int H, int N, int d,
  *   alpha_q, alpha_k  [B, H, N] fp32 from binattn_pack, device, read.
  *   bias              [H, N, N] bf16 or NULL (= zero), device, read. Shared by
  *                     every batch index b. Added after scaling; not scaled.
+ *                     It may hold -inf (a mask): such a pair has no weight, and
+ *                     a query whose row holds nothing else gets a result of 0.
+ *                     A row of the type's lowest value gets uniform weights, as
+ *                     in the formula; below -2^30 the scores count for nothing
+ *                     beside the bias. (A row without any bias above -2^30 takes
+ *                     a pass of its own over the keys, several times as long.)
  *   v                 [B, H, N, d] bf16, device, read.
  *   softmax_scale     finite float (usually 1/sqrt(d)).
  *   out               [B, H, N, d] bf16, device, written (round to nearest even
@@ -130,7 +136,8 @@ int binattn_pack(const void *x, int dtype, int B, int H, int N, int d,
  * Numerics: S exact (integer); logits and softmax in fp32; P rounded to bf16
  * before a bf16 x bf16 -> fp32 P.V on the tensor-core engines (fp32 P on SIMT);
  * normalisation by the fp32 row sum in the epilogue.
- * No mask: every query attends to all N keys (vision / diffusion self-attention).
+ * No mask but the bias: without one every query attends to all N keys (vision /
+ * diffusion self-attention).
  * Speed: for d % 8 == 0, d <= 80 this runs the TMA-fed tensor-core pipeline,
  * except with a bias whose rows are not a multiple of 8 elements (N % 8 != 0,
  * e.g. N = 197 or 577): TMA cannot read such rows, so that call reads the bias
@@ -295,7 +302,7 @@ int binattn_quantize_v(const uint16_t *v, int B, int H, int N, int d, int8_t *vq
 
 /*
  * binattn_forward_int8 — the forward with an 8-bit P.V, the pages' hybrid
- * variant: the scores, scale and bias as in binattn_forward; then
+ * variant: the scores, scale and bias (here finite) as in binattn_forward; then
  * u_ij = rint(255 * exp(logit_ij - max_j logit_ij)) (attention coefficients on
  * [0, 1] in a static unsigned 8-bit code), V in its per-channel 8-bit code
  * (binattn_quantize_v), and O[b,h,i,c] = scale[b,h,c] * sum_j u_ij vq_jc /
@@ -357,7 +364,7 @@ int binattn_forward_sample_bias_ws(const uint32_t *q_bits, const uint32_t *k_bit
  * i and patch key j is table[h, (y_i - y_j + gh - 1)(2 gw - 1) + x_i - x_j +
  * gw - 1]; a class query with a patch key takes table[h, R0], a patch query
  * with a class key table[h, R0 + 1], class with class table[h, R0 + 2].
- *   table      bf16 [H, R0 + 3 n_cls], device, 16-byte aligned; at most
+ *   table      bf16 [H, R0 + 3 n_cls], device, 16-byte aligned, finite; at most
  *              20480 entries per head (BINATTN_ERR_UNSUPPORTED beyond).
  *   workspace  at least binattn_forward_relpos_workspace_bytes(...) bytes
  *              (the split tail's partials; may be NULL when that is 0).
@@ -387,7 +394,10 @@ int binattn_forward_relpos(const uint32_t *q_bits, const uint32_t *k_bits,
  * The gradient stops at s and t: how it reaches q and k through sign and the
  * mean (the estimator of quantisation-aware training) is the caller's choice;
  * with the straight-through estimator dq = ds and dk = dt.
- *   q_bits, k_bits, alpha_q, alpha_k, bias, v   as binattn_forward.
+ *   q_bits, k_bits, alpha_q, alpha_k, bias, v   as binattn_forward, but the bias
+ *          finite, and in every row with a value above -1e4 or so: the row's
+ *          log-sum-exp is one fp32 number, which has no room for the sum beside
+ *          a larger one. binattn_backward_bf16 takes rows that are masked out.
  *   dO     bf16 [B, H, N, d], device.
  *   dV, ds, dt   fp32 [B, H, N, d], device, written.
  *   dbias  fp32 [H, N, N], device, written (the gradient of a zero bias when
@@ -415,10 +425,11 @@ int binattn_backward(const uint32_t *q_bits, const uint32_t *k_bits,
  * steps. P and dlogit (times the other side's alpha) are rounded to bf16 before
  * their products, which accumulate in fp32; the softmax statistics, D and the
  * sum over b stay in fp32; every gradient is rounded once.
- *   q_bits ... dO   as binattn_backward. The bias may hold -inf (a mask): such
- *                   a pair has no weight, and a query whose row holds nothing
- *                   else passes no gradient on. With rows of the type's lowest
- *                   value instead the weights are uniform, as in the formula.
+ *   q_bits ... dO   as binattn_forward has them, masks in the bias included: a
+ *                   pair at -inf has no weight, and a query whose row holds
+ *                   nothing else (its result is 0) passes no gradient on. With
+ *                   rows of the type's lowest value instead the weights are
+ *                   uniform, as in the formula.
  *   dV, ds, dt      bf16 [B, H, N, d], device, written.
  *   dbias           bf16 [H, N, N], device, written, or NULL.
  *   workspace       device, 16-byte aligned, at least
@@ -579,7 +590,8 @@ int binattn_scores_debug(const uint32_t *q_bits, const uint32_t *k_bits,
  * binattn_ref_bf16_forward — full-precision softmax attention on the same
  * shapes, the speed reference the binary kernel is compared against:
  * O = softmax(softmax_scale * Q K^T + bias) V with bf16 Q, K, V, bias (NULL =
- * zero), fp32 accumulation and softmax, bf16 output. Needs d % 8 == 0.
+ * zero; masks as binattn_forward's), fp32 accumulation and softmax, bf16
+ * output. Needs d % 8 == 0.
  */
 int binattn_ref_bf16_forward(const uint16_t *q, const uint16_t *k,
                              const uint16_t *bias, const uint16_t *v,
