@@ -40,6 +40,7 @@ namespace nr {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxBlocks = 148 * 3;  // per tensor of a launch (blocks_for)
 
 // Both tensors (index 0: q, 1: k; blockIdx.y) of one call. Strides in elements.
 struct Params {
@@ -117,21 +118,16 @@ __device__ __forceinline__ bool nonneg_exact(float xa, float wa, float c, float 
   return a != b ? a > b : __fma_rn(u, cd, -a) >= __fma_rn(v, sd, -b);
 }
 
-// The token of row i (batch, token, head with the head fastest).
+// The token of row i (batch, token, head with the head fastest). Callers hold B * H
+// and N to 65535, so every row, and a round's step beyond the last, fits 32 bits.
+static_assert(65535ull * 65535 + kMaxBlocks * kWarps * 32ull <= 0xffffffffull, "rows are numbered in 32 bits");
 struct Row {
   int b, h, n;
 };
-__device__ __forceinline__ Row row_of(unsigned long long i, int H, int N, bool small) {
+__device__ __forceinline__ Row row_of(unsigned i, int H, int N) {
   Row w;
-  unsigned tk;  // batch * N + token < 2^32
-  if (small) {
-    const unsigned u = static_cast<unsigned>(i);
-    tk = u / static_cast<unsigned>(H);
-    w.h = static_cast<int>(u - tk * static_cast<unsigned>(H));
-  } else {
-    tk = static_cast<unsigned>(i / static_cast<unsigned>(H));
-    w.h = static_cast<int>(i % static_cast<unsigned>(H));
-  }
+  const unsigned tk = i / static_cast<unsigned>(H);  // batch * N + token
+  w.h = static_cast<int>(i - tk * static_cast<unsigned>(H));
   w.b = static_cast<int>(tk / static_cast<unsigned>(N));
   w.n = static_cast<int>(tk - static_cast<unsigned>(w.b) * static_cast<unsigned>(N));
   return w;
@@ -200,12 +196,12 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_rows_kernel(const Param
 #pragma unroll
     for (int e = 0; e < 4; ++e) dwf[k][e] = dws[k][e] = 0.f;
 
-  const unsigned long long rows = static_cast<unsigned long long>(p.B) * H * N;
+  const unsigned rows = static_cast<unsigned>(p.B) * H * N;
   const float inv_d = 1.f / static_cast<float>(d);
-  const unsigned step = gridDim.x * kWarps * rpw;  // rows per round, below 2^32
-  const Row by = row_of(step, H, N, true);         // ... as batch entries, tokens, heads
-  unsigned long long i = (static_cast<unsigned long long>(blockIdx.x) * kWarps + warp) * rpw + grp;
-  Row w = row_of(i, H, N, true);
+  const unsigned step = gridDim.x * kWarps * rpw;  // rows per round
+  const Row by = row_of(step, H, N);               // ... as batch entries, tokens, heads
+  unsigned i = (blockIdx.x * kWarps + warp) * rpw + grp;
+  Row w = row_of(i, H, N);
   // A row's x (and dz) are loaded, as they lie in memory, while the row before is
   // worked on: the bytes that are under way bound the pass.
   Quad<T> xq[2 * kC];
@@ -227,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_rows_kernel(const Param
   };
   if (live && i < rows) fetch(w);
   // the trip count is warp-uniform: by the warp's first row
-  for (unsigned long long i0 = i - grp; i0 < rows; i0 += step, i += step) {
+  for (unsigned i0 = i - grp; i0 < rows; i0 += step, i += step) {
     const bool in = live && i < rows;
     float xf[kC][4], xs[kC][4], cs[kC][4], sn[kC][4], zf[kC][4], zs[kC][4];
     const size_t row = (static_cast<size_t>(w.b) * H + w.h) * N + w.n;
@@ -418,8 +414,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const Params p,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* x = static_cast<const T*>(p.x[t]);
   const float* wt = p.w[t];
-  const unsigned long long rows = static_cast<unsigned long long>(p.B) * H * N;
-  const bool small = rows <= 0xffffffffull;
+  const unsigned rows = static_cast<unsigned>(p.B) * H * N;
   const float inv_d = 1.f / static_cast<float>(d);
   float dw[4] = {0.f, 0.f, 0.f, 0.f};
   auto all_sum = [](float v) {
@@ -427,9 +422,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const Params p,
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   };
-  for (unsigned long long i = static_cast<unsigned long long>(blockIdx.x) * kWarps + warp; i < rows;
-       i += static_cast<unsigned long long>(gridDim.x) * kWarps) {
-    const Row w = row_of(i, H, N, small);
+  for (unsigned i = blockIdx.x * kWarps + warp; i < rows; i += gridDim.x * kWarps) {
+    const Row w = row_of(i, H, N);
     const T* src = x + w.b * p.xb[t] + w.h * p.xh[t] + w.n * p.xn[t];
     const size_t row = (static_cast<size_t>(w.b) * H + w.h) * N + w.n;
     const size_t tok = (p.per_batch ? static_cast<size_t>(w.b) * N : 0) + w.n;
@@ -542,7 +536,6 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* __restri
 // Blocks per tensor of a launch: one round of rows, at most 3 blocks per SM of a
 // 148-SM part and tensor (the kernels stride over the rest; the backward writes
 // one row of partial sums per block).
-constexpr int kMaxBlocks = 148 * 3;
 inline int blocks_for(unsigned long long rows, int rows_per_block) {
   const unsigned long long b = (rows + rows_per_block - 1) / rows_per_block;
   return b < kMaxBlocks ? static_cast<int>(b) : kMaxBlocks;
