@@ -405,10 +405,13 @@ def _backward_buffers(shape, dev, with_dbias, need, workspace, stream):
 
 def backward_bf16(q_bits: torch.Tensor, k_bits: torch.Tensor, alpha_q: torch.Tensor, alpha_k: torch.Tensor,
                   bias: torch.Tensor | None, v: torch.Tensor, dO: torch.Tensor, softmax_scale: float,
-                  with_dbias: bool = True, workspace: torch.Tensor | None = None, stream=None):
+                  with_dbias: bool | None = None, workspace: torch.Tensor | None = None, stream=None):
     """backward on the tensor cores: (dV, ds, dt, dbias) in bf16. Needs d % 8 == 0;
-    a bias may hold -inf (binattn_backward_bf16). workspace: uint8 CUDA tensor of at
-    least backward_bf16_workspace_bytes(...) bytes, allocated here when None."""
+    a bias may hold -inf (binattn_backward_bf16). with_dbias None: where there is a
+    bias (True gives the gradient of a zero bias, too: [H,N,N] and a kernel of its
+    own). workspace: uint8 CUDA tensor of at least backward_bf16_workspace_bytes(...)
+    bytes, allocated here when None."""
+    with_dbias = bias is not None if with_dbias is None else with_dbias
     B, H, N, d = v.shape
     _expect(dO, "dO", (B, H, N, d), (torch.bfloat16,))
     dev = _forward_args(q_bits, k_bits, alpha_q, alpha_k, bias, v, None)
@@ -428,11 +431,13 @@ def backward_bf16_workspace_bytes(B: int, H: int, N: int, d: int, has_bias: bool
 
 
 def ref_bf16_backward(q: torch.Tensor, k: torch.Tensor, bias: torch.Tensor | None, v: torch.Tensor, dO: torch.Tensor,
-                      softmax_scale: float, with_dbias: bool = True, workspace: torch.Tensor | None = None,
+                      softmax_scale: float, with_dbias: bool | None = None, workspace: torch.Tensor | None = None,
                       stream=None):
     """Gradients of ref_bf16_forward for an upstream gradient dO (bf16 [B,H,N,d]):
     (dq, dk, dv, dbias) in bf16, dbias [H,N,N] summed over the batch, or None without
-    with_dbias. The probabilities are computed again from q and k."""
+    with_dbias (None: as backward_bf16). The probabilities are computed again from q
+    and k."""
+    with_dbias = bias is not None if with_dbias is None else with_dbias
     B, H, N, d = q.shape
     for name, t in (("q", q), ("k", k), ("v", v), ("dO", dO)):
         _expect(t, name, (B, H, N, d), (torch.bfloat16,))
