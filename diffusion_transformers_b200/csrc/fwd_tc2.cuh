@@ -230,59 +230,91 @@ __device__ __forceinline__ uint32_t e4m3_bytes(uint32_t word, int j0, int c0, in
 }
 
 // The result of a row without any logit above kNone (which is all that the key loop
-// weighs; of other rows it is left alone). Biases that low are 64 or more apart in
-// fp32 and the scores vanish beside them, so the weights are 1 where the row's bias
+// weighs; other rows are left alone). Biases that low are 64 or more apart in fp32
+// and the scores vanish beside them, so the weights are 1 where the row's bias
 // (brow, of the CTA's keys) is largest and 0 elsewhere, and none at -inf: then the
 // result is 0. Written to orow or, for a key half, to part (values 2 kRows apart: the
-// sum, its max, the sum of the weights). It runs behind everything else: inside the
-// key loop or its epilogue the same work cost ordinary rows 1 to 7% (283.8 us at 2 x
-// 16 x 4096 x 72 with this; 290 to 304 in the loop).
-__device__ __forceinline__ void masked_row(const uint16_t* brow, const uint16_t* v, int keys, int d, uint16_t* orow,
-                                        float* part) {
-  // the biases of keys j .. j + 7 (rows are padded to a multiple of 8)
-  auto load = [&](int j, float (&b)[8]) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(brow + j));
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-      b[e] = j + e < keys ? x : -INFINITY;
-    }
+// sum, its max, the sum of the weights). A warp calls it together, a lane per row
+// (valid: there is one). It runs behind everything else: inside the key loop or its
+// epilogue the same work cost ordinary rows 1 to 7% (283.8 us at 2 x 16 x 4096 x 72
+// with this; 290 to 304 in the loop). There, on the device, 277 us without
+// such rows; with an eighth of them at -inf 395, at the lowest value in all keys 560,
+// and 4.4 ms where a row holds both.
+__device__ __forceinline__ void masked_rows(const uint16_t* brow, const uint16_t* v, int keys, int d, uint16_t* orow,
+                                            float* part, bool valid) {
+  // Many loads at a time: a row is a chain of its own, with few beside it.
+  auto bias8 = [&](int j) {  // the biases of keys j .. j + 7 (rows are padded to a multiple of 8)
+    return j < keys ? __ldg(reinterpret_cast<const uint4*>(brow + j)) : make_uint4(0, 0, 0, 0);
   };
-  float top = -INFINITY, n = 0.f, b[8];
-  for (int j = 0; j < keys; j += 8) {
-    load(j, b);
+  auto bf = [](const uint4& b, int e) {
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+    return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+  };
+  float top = -INFINITY, bottom = INFINITY;
+  for (int j0 = 0; valid && j0 < keys; j0 += 128) {
+    uint4 b[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, b[e]);
-    if (top > kNone) return;
-  }
-  for (int c = 0; c < d; c += 8) {
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    n = 0.f;
-    for (int j = 0; j < keys && top > -INFINITY; j += 8) {
-      load(j, b);
+    for (int u = 0; u < 16; ++u) b[u] = bias8(j0 + 8 * u);
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (b[e] == top) {
-          n += 1.f;
-          const uint4 raw = __ldg(reinterpret_cast<const uint4*>(v + static_cast<size_t>(j + e) * d + c));
-          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        if (j0 + 8 * u + e < keys) {
+          top = fmaxf(top, bf(b[u], e));
+          bottom = fminf(bottom, bf(b[u], e));
+        }
+      }
+    valid = top <= kNone;
+  }
+  // Rows alike in all keys take V's sums, which the lanes form together; the
+  // others each their own.
+  const bool any = valid && top > -INFINITY, alike = any && top == bottom;
+  const bool sums = __any_sync(0xffffffffu, alike);
+  const int lane = threadIdx.x & 31;
+  float n = alike ? static_cast<float>(keys) : 0.f;
+  for (int c = 0; c < d; c += 8) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (sums) {
+      for (int j = lane; j < keys; j += 32) {
+        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(v + static_cast<size_t>(j) * d + c));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] += __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+        for (int k = 0; k < 8; ++k) o[k] += bf(raw, k);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        for (int s = 16; s; s >>= 1) o[k] += __shfl_xor_sync(0xffffffffu, o[k], s);
+    }
+    if (!alike) {
+      n = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = 0.f;
+      for (int j = 0; any && j < keys; j += 16) {
+        const uint4 b[2] = {bias8(j), bias8(j + 8)};
+        uint4 raw[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          raw[e] = __ldg(reinterpret_cast<const uint4*>(v + static_cast<size_t>(min(j + e, keys - 1)) * d + c));
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const bool on = j + e < keys && bf(b[e >> 3], e & 7) == top;
+          n += on ? 1.f : 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] += on ? bf(raw[e], k) : 0.f;
         }
       }
     }
+    if (!valid) continue;
     if (part) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) part[(c + k) * (2 * kRows)] = o[k];
     } else {
-      const float inv = n > 0.f ? 1.f / n : 0.f;
+      const float inv = any ? 1.f / n : 0.f;
       *reinterpret_cast<uint4*>(orow + c) =
           make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
                      pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
     }
   }
-  if (part) {
+  if (valid && part) {
     part[d * (2 * kRows)] = top;
     part[(d + 1) * (2 * kRows)] = n;
   }
@@ -696,7 +728,7 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
     float ci = 0.f;
     // A dense bias may leave a row, or its first keys, with nothing but masked
     // logits: while a row has none above kNone, m stays there (finite, so that no
-    // -inf becomes an offset) and its weights are 0; see masked_row.
+    // -inf becomes an offset) and its weights are 0; see masked_rows.
     constexpr float kTop = kMasks ? kNone : -INFINITY;
     float m = kTop;
     bool ok = true;
@@ -1020,7 +1052,7 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
         uint32_t lbits;  // l = O_t column d
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(lbits) : "r"(o_col + d));
         tmem_ld_wait();
-        if (kMasks && lbits == 0u) *masked = 1;  // masked_row writes this row again
+        if (kMasks && lbits == 0u) *masked = 1;  // masked_rows writes this row again
         if (p.split) {
           // Partial result of this key half: unnormalised O (d fp32), then m, then l.
           // channel-major: value c of row r256 of (pair slot, half) at
@@ -1089,12 +1121,12 @@ fwd_tc2_kernel(const tc::Params p, const __grid_constant__ CUtensorMap tm_v,
       for (int it = 0; it < n_items; ++it) {
         const Item w = item(it);
         const int row = w.q0 + static_cast<int>(threadIdx.x);
-        if (row >= N) continue;
         const size_t slice = p.bias_per_sample ? w.bh : w.h;
         const uint16_t* brow = p.bias + (slice * N + row) * (p.bias_ld > 0 ? p.bias_ld : N) + key0;
         float* part = p.split ? p.part + static_cast<size_t>((blockIdx.x >> 1) * 2 + half) * (d + 2) * (2 * kRows) + threadIdx.x
                               : nullptr;
-        masked_row(brow, p.v + (w.tok0 + key0) * d, min(N - key0, nkt * kKeys), d, p.out + (w.tok0 + row) * d, part);
+        masked_rows(brow, p.v + (w.tok0 + key0) * d, min(N - key0, nkt * kKeys), d, p.out + (w.tok0 + row) * d, part,
+                    row < N);
       }
     }
   }

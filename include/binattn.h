@@ -127,8 +127,9 @@ int binattn_pack(const void *x, int dtype, int B, int H, int N, int d,
  *                     a query whose row holds nothing else gets a result of 0.
  *                     A row of the type's lowest value gets uniform weights, as
  *                     in the formula; below -2^30 the scores count for nothing
- *                     beside the bias. (A row without any bias above -2^30 takes
- *                     a pass of its own over the keys, several times as long.)
+ *                     beside the bias. (Rows without any bias above -2^30 take a
+ *                     pass of their own over the keys; slow where such a row is
+ *                     not alike in all keys.)
  *   v                 [B, H, N, d] bf16, device, read.
  *   softmax_scale     finite float (usually 1/sqrt(d)).
  *   out               [B, H, N, d] bf16, device, written (round to nearest even
