@@ -18,7 +18,8 @@
 //    the batch innermost: dL summed over b in fp32 registers, rounded once.
 // Every sum has one owner and one order, so there are no atomics and the same
 // call gives the same bits. The price against one kernel that adds dQ with
-// atomics is two more score products and exps.
+// atomics is two more score products, two more products dP and two more rounds of
+// exps: 9 products instead of 5 (with dbias 11).
 //
 // The three share one machine. tile_kernel first lays q, k, v and dO (binary: the
 // signs of q and k as +-1) out as the tensor cores take them: tiles of 64 rows,
@@ -239,7 +240,7 @@ __device__ __forceinline__ void logits(uint32_t* s, const float* ak, float ci, c
 // 2^y of two values (y <= 1 or so) without the special-function unit: y = n + f
 // with n the nearest integer (added to 1.5 * 2^23 it stands in the low bits of
 // the sum), 2^f by a polynomial fitted to the smallest relative error on [-1/2,
-// 1/2] with constant term 1 (9.2e-8, in fp32 1.6e-7: no worse than ex2.approx),
+// 1/2] with constant term 1 (1.08e-7, in fp32 1.7e-7: no worse than ex2.approx),
 // and n added to the exponent. y is cut off at -127, where f is 0 and the
 // result's bits are all 0: masked pairs keep a weight of exactly 0.
 __device__ __forceinline__ float2 ex2_fma(float2 y) {
@@ -271,7 +272,7 @@ __device__ __forceinline__ float2 exp2v(float2 x, float2 minus_top, float2 minus
 }
 // Without a bias every fourth pair of a row's exps runs on the FMA pipe, which has
 // room there beside the special-function unit: 767 against 785 us at 2 x 16 x
-// 4096 x 72 (every second 830, every eighth 773). With a bias the FMA pipe has
+// 4096 x 72 on the same inputs again and again (every second 830, every eighth 773). With a bias the FMA pipe has
 // its share of the logits too, and taking none is best: 1487 against 1510 us.
 template <bool kBias>
 __device__ __forceinline__ constexpr bool on_fma(int pair) { return !kBias && pair % 4 == 3; }

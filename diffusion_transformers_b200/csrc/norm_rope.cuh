@@ -25,13 +25,17 @@
 // the rows a block works on share a few tokens' tables. Shapes outside d % 8 ==
 // 0, R % 8 == 0 and 4-element alignment take one warp per row and scalar loads.
 //
-// Measured on one B200 (copies 6.5 TB/s), bf16, 2 x 16 x 4096 x 72 with R = 72, q
-// and k: 31 us, 2.5 TB/s; backward 53 us, 2.2 TB/s, and 6 us for the sums of dw
-// over the blocks. Sign bits at 8 x 16 x 1024 x 72: 38 us (770 instructions per
-// warp for ten rows, half of the issue slots used). What bounds it is issue and
-// latency with 16 warps per SM (128 registers for three chunks and their
-// angles); held to 80 registers, for three blocks per SM, it gained nothing. One
-// token of 16 heads: 4 us, a launch.
+// Measured on one B200 (copies 6.5 TB/s) on the device (replayed graphs, inputs
+// above L2), 2 x 16 x 4096 x 72 with R = 72, q and k: bf16 29 us, 2.6 TB/s; fp32 36 us,
+// 4.2 TB/s; the gradient in bf16 52 us, 6 of them the sums of dw over the blocks, in
+// fp32 85 us. Sign bits at 8 x 16 x 1024 x 72, bf16, interleaved: 37 us (770
+// instructions per warp for ten rows, half of the issue slots used), against 40 for
+// the norm and rotation followed by two packs; fp32 47 against 74, but bf16 in split
+// pairs 40 against 39. What bounds it is issue and latency with 16 warps per SM
+// (128 registers for three chunks and their angles); held to 80 registers, for
+// three blocks per SM, it gained nothing. The gradient spills at three chunks (24 to
+// 220 bytes a thread). The scalar kernel (rot = 36 of 72): 111 us, sign bits 122,
+// gradient 150. One token of 16 heads: 2.2 us, a launch.
 #pragma once
 #include "common.cuh"
 
