@@ -235,9 +235,9 @@ __device__ __forceinline__ uint32_t e4m3_bytes(uint32_t word, int j0, int c0, in
 // (brow, of the CTA's keys) is largest and 0 elsewhere, and none at -inf: then the
 // result is 0. Written to orow or, for a key half, to part (values 2 kRows apart: the
 // sum, its max, the sum of the weights). A warp calls it together, a lane per row
-// (valid: there is one). It runs behind everything else: inside the key loop or its
-// epilogue the same work cost ordinary rows 1 to 7% (283.8 us at 2 x 16 x 4096 x 72
-// with this; 290 to 304 in the loop). There, on the device, 277 us without
+// (valid: there is one). It runs behind everything else: inside the key loop the
+// same work cost ordinary rows 2 to 8% (290 to 309 us at 2 x 16 x 4096 x 72 instead of
+// 284 to 287, as without it). There, on the device, 277 us without
 // such rows; with an eighth of them at -inf 395, at the lowest value in all keys 560,
 // and 4.4 ms where a row holds both.
 __device__ __forceinline__ void masked_rows(const uint16_t* brow, const uint16_t* v, int keys, int d, uint16_t* orow,
